@@ -48,6 +48,13 @@ _SIGS = {
     "hca_compress_attn_decode": ([_vp] * 4 + [_i32, _i32] + [_vp] * 6 + [_i32, _i32, _i32, _i32, _i64, _i32, _f32, _i32,
                                                                       _vp, _vp, _vp, _sz, _vp], _i32),
     "sparse_attn_decode_noalloc": ([_vp] * 6 + [_i32, _i32, _i32, _i32, _i64, _i32, _i32, _f32, _i32, _vp, _vp, _vp], _i32),
+    "latent_append_paged": ([_vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _i32,
+                             _vp, _i64, _i64, _vp, _i32, _i32, _i32, _vp], _i32),
+    "attn_decode_paged_workspace_size": ([_i32, _i32, _i32, _i64], _sz),
+    "hca_attn_decode_paged": ([_vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp] + [_i32] * 5 +
+                              [_f32, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
+    "sparse_attn_decode_paged": ([_vp, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp] + [_i32] * 5 +
+                                 [_f32, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
     "sparse_attn_prefill": ([_vp] * 5 + [_i64, _vp, _vp] + [_i32] * 5 + [_i64, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _sz, _vp], _i32),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -309,3 +316,111 @@ def sparse_attn_decode_noalloc(q, cache, idx, win, win_len, sink, sm_scale, d_v,
     _check(lib.sparse_attn_decode_noalloc(_p(q), _p(cache), _p(idx), _p(win), _p(win_len), _p(sink), B, H, d_k,
                                           d_v, cache.shape[1], k, W, sm_scale, _dtype_code(q), _p(out), _p(lse),
                                           _stream(stream)), "sparse_attn_decode_noalloc")
+
+
+# ---- paged cache.  The tensors' shapes, types, strides and device are checked here (the C
+# calls see addresses only): what does not fit raises CsaError and nothing is launched.
+def _want(name, what, t, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise CsaError(f"{name}: {what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                       f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _paged(name, pages, block_table):
+    """Checks of the pool and its table; the device of the call."""
+    dev = pages.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise CsaError(f"{name}: pages must be on the current CUDA device, got {dev}")
+    if pages.dim() != 3 or not pages.is_contiguous() or pages.dtype not in (torch.bfloat16, torch.float32):
+        raise CsaError(f"{name}: pages must be a contiguous bf16 or fp32 tensor [n_pages, page_size, d]")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev or not block_table.is_contiguous():
+        raise CsaError(f"{name}: block_table must be a contiguous int32 tensor [B, table_width] on {dev}")
+    return dev
+
+
+def latent_append_paged(rows, entry, pages, block_table, seq=None, pos=None, inv_freq=None, interleaved=True, q_pe=None,
+                        q=None, stream=None):
+    """Append rows [T, d] to the paged cache, row t at entry entry[t] of sequence seq[t] (seq None:
+    sequence t), the last 2 * len(inv_freq) values rotated by pos[t] (None: entry[t]) * inv_freq; the
+    rotary parts q_pe [T, H, d_r] rotated into the last d_r values of q [T, H, d_q].  rows and q_pe may
+    be strided in all but their last dimension.  See csa.h."""
+    name = "latent_append_paged"
+    dev = _paged(name, pages, block_table)
+    n_pages, page, d = pages.shape
+    B, width = block_table.shape
+    T = entry.shape[0] if entry.dim() == 1 else -1
+    dt = pages.dtype
+    _want(name, "entry", entry, torch.int32, (T,), dev)
+    if rows.shape != (T, d) or rows.dtype != dt or rows.device != dev or (d > 1 and rows.stride(1) != 1):
+        raise CsaError(f"{name}: rows must be [{T}, {d}] {dt} on {dev} with a dense last dimension")
+    if seq is not None:
+        _want(name, "seq", seq, torch.int32, (T,), dev)
+    if pos is not None:
+        _want(name, "pos", pos, torch.int32, (T,), dev)
+    d_r = 0
+    if inv_freq is not None:
+        d_r = 2 * inv_freq.numel()
+        _want(name, "inv_freq", inv_freq, torch.float32, (d_r // 2,), dev)
+    H = d_q = ld_t = ld_h = 0
+    if (q is None) != (q_pe is None):
+        raise CsaError(f"{name}: q and q_pe come together")
+    if q is not None:
+        H, d_q = (q.shape[1], q.shape[2]) if q.dim() == 3 else (-1, -1)
+        _want(name, "q", q, dt, (T, H, d_q), dev)
+        if q_pe.shape != (T, H, d_r) or q_pe.dtype != dt or q_pe.device != dev or q_pe.stride(2) != 1:
+            raise CsaError(f"{name}: q_pe must be [{T}, {H}, {d_r}] {dt} on {dev} with a dense last dimension")
+        ld_t, ld_h = q_pe.stride(0), q_pe.stride(1)
+    ld = rows.stride(0) if T > 1 else d
+    _check(lib.latent_append_paged(rows.data_ptr(), ld, _p(seq), entry.data_ptr(), _p(pos), _p(inv_freq), d_r,
+                                   int(interleaved), pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, B, T,
+                                   d, _p(q_pe), ld_t, ld_h, _p(q), H, d_q, _dtype_code(pages), _stream(stream)), name)
+
+
+def attn_decode_paged_workspace_size(B, H, d_v, rows_max):
+    return int(lib.attn_decode_paged_workspace_size(B, H, d_v, rows_max))
+
+
+def _paged_attn(name, q, pages, block_table, sel, sel_shape, win, win_len, sink, d_v, out, lse, workspace):
+    """Checks of a paged attention call; (B, H, d_k, W, workspace address, bytes)."""
+    dev = _paged(name, pages, block_table)
+    d_k = pages.shape[2]
+    B = block_table.shape[0]
+    H = q.shape[1] if q.dim() == 3 else -1
+    dt = pages.dtype
+    _want(name, "q", q, dt, (B, H, d_k), dev)
+    _want(name, "out", out, dt, (B, H, d_v), dev)
+    _want(name, "sink", sink, torch.float32, (H,), dev)
+    _want(name, "n_entries" if len(sel_shape) == 1 else "idx", sel, torch.int32, sel_shape, dev)
+    W = 0
+    if win is not None:
+        W = win.shape[1] if win.dim() == 3 else -1
+        _want(name, "win", win, dt, (B, W, d_k), dev)
+        _want(name, "win_len", win_len, torch.int32, (B,), dev)
+    if lse is not None:
+        _want(name, "lse", lse, torch.float32, (B, H), dev)
+    if workspace is None or workspace.device != dev or not workspace.is_contiguous():
+        raise CsaError(f"{name}: workspace must be a contiguous tensor on {dev}")
+    return B, H, d_k, W, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def hca_attn_decode_paged(q, pages, block_table, n_entries, win, win_len, sink, sm_scale, d_v, out, lse=None,
+                          workspace=None, stream=None):
+    """hca_attn_decode over a paged cache: pages [n_pages, page_size, d_k], block_table [B, table_width]."""
+    B, H, d_k, W, wp, wb = _paged_attn("hca_attn_decode_paged", q, pages, block_table, n_entries, block_table.shape[:1],
+                                       win, win_len, sink, d_v, out, lse, workspace)
+    _check(lib.hca_attn_decode_paged(q.data_ptr(), pages.data_ptr(), pages.shape[0], pages.shape[1],
+                                     block_table.data_ptr(), block_table.shape[1], n_entries.data_ptr(), _p(win),
+                                     _p(win_len), sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, _dtype_code(q),
+                                     out.data_ptr(), _p(lse), wp, wb, _stream(stream)), "hca_attn_decode_paged")
+
+
+def sparse_attn_decode_paged(q, pages, block_table, idx, win, win_len, sink, sm_scale, d_v, out, lse=None,
+                             workspace=None, stream=None):
+    """sparse_attn_decode over a paged cache: idx [B, k] entry ids (-1 = unused slot)."""
+    k = idx.shape[1] if idx.dim() == 2 else -1
+    B, H, d_k, W, wp, wb = _paged_attn("sparse_attn_decode_paged", q, pages, block_table, idx,
+                                       (block_table.shape[0], k), win, win_len, sink, d_v, out, lse, workspace)
+    _check(lib.sparse_attn_decode_paged(q.data_ptr(), pages.data_ptr(), pages.shape[0], pages.shape[1],
+                                        block_table.data_ptr(), block_table.shape[1], idx.data_ptr(), k, _p(win),
+                                        _p(win_len), sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, _dtype_code(q),
+                                        out.data_ptr(), _p(lse), wp, wb, _stream(stream)), "sparse_attn_decode_paged")

@@ -7,6 +7,7 @@
 
 #include "attention.cuh"
 #include "indexer.cuh"
+#include "paged.cuh"
 
 namespace csa {
 cudaError_t launch_csa_compress(const void*, const void*, const void*, const void*, const float*, const float*,
@@ -35,6 +36,9 @@ cudaError_t launch_window_append(const void*, void*, const int32_t*, int, int, i
 cudaError_t launch_index_key_compress(const void*, const void*, const void*, const void*, const float*,
                                       const float*, const void*, const void*, const int32_t*, void*, void*, int64_t,
                                       int, int, int, int, int, cudaStream_t, unsigned*);
+cudaError_t launch_latent_append_paged(const void*, int64_t, const int32_t*, const int32_t*, const int32_t*, const float*,
+                                       int, int, void*, int64_t, int, const int32_t*, int, int, int, int, const void*,
+                                       int64_t, int64_t, void*, int, int, int, cudaStream_t, unsigned*);
 }  // namespace csa
 
 using namespace csa;
@@ -689,6 +693,97 @@ csa_status sparse_attn_prefill(const void* q, const int32_t* q_pos, const void* 
   a.raw_pos0 = raw_pos0; a.t_raw = t_raw; a.W = W; a.prefill = 1; a.sink = sink; a.B = B; a.Tq = Tq; a.H = H;
   a.dk = d_k; a.dv = d_v; a.n_max = n_max; a.sm_scale = sm_scale; a.out = out; a.lse = lse; a.err = err;
   return run_attention(a, dtype, workspace, ws_bytes, false, S(stream));
+}
+
+// ----------------------------------------------------------------------------- paged cache
+static csa_status paged_checks(const void* pages, int64_t n_pages, int page_size, const int32_t* block_table,
+                               int table_width, int B) {
+  REQUIRE(B >= 1 && B <= 65535 && n_pages >= 1 && page_size >= 1 && page_size <= 65536 && table_width >= 1, CSA_ERR_SHAPE);
+  // entry ids and pool rows fit 31 bits
+  REQUIRE((int64_t)table_width * page_size <= 0x7fffffffLL && n_pages <= 0x7fffffffLL / page_size, CSA_ERR_SHAPE);
+  REQUIRE_PTR(pages);
+  REQUIRE(block_table, CSA_ERR_NULL);
+  return CSA_OK;
+}
+
+csa_status latent_append_paged(const void* rows, int64_t rows_ld, const int32_t* seq, const int32_t* entry,
+                               const int32_t* pos, const float* inv_freq, int d_r, int interleaved, void* pages,
+                               int64_t n_pages, int page_size, const int32_t* block_table, int table_width, int B,
+                               int T, int d, const void* q_pe, int64_t qpe_ld_t, int64_t qpe_ld_h, void* q, int H,
+                               int d_q, int dtype, void* stream) {
+  REQUIRE(dtype == CSA_F32 || dtype == CSA_BF16, CSA_ERR_DTYPE);
+  const int vec = dtype == CSA_BF16 ? 8 : 4;
+  csa_status s = paged_checks(pages, n_pages, page_size, block_table, table_width, B);
+  if (s != CSA_OK) return s;
+  REQUIRE(T >= 1 && d >= 1 && d <= 576 && d % vec == 0 && rows_ld >= d && rows_ld % vec == 0, CSA_ERR_SHAPE);
+  REQUIRE(seq || T <= B, CSA_ERR_SHAPE);
+  REQUIRE_PTR(rows);
+  REQUIRE(entry, CSA_ERR_NULL);
+  if (inv_freq) {
+    REQUIRE(d_r >= 1 && d_r <= d && d_r % ((interleaved ? 1 : 2) * vec) == 0, CSA_ERR_SHAPE);
+  } else {
+    REQUIRE(d_r == 0, CSA_ERR_NULL);
+  }
+  if (q) {
+    REQUIRE(d_r > 0, CSA_ERR_NULL);
+    REQUIRE(H >= 1 && H <= 128 && d_q >= d_r && d_q % vec == 0, CSA_ERR_SHAPE);
+    REQUIRE(qpe_ld_t % vec == 0 && qpe_ld_h % vec == 0 && qpe_ld_t >= 0 && qpe_ld_h >= 0, CSA_ERR_SHAPE);
+    REQUIRE_PTR(q); REQUIRE_PTR(q_pe);
+  }
+  unsigned* err = device_error_word();
+  REQUIRE(err, CSA_ERR_CUDA);
+  return cuda_status(launch_latent_append_paged(rows, rows_ld, seq, entry, pos, inv_freq, d_r, interleaved != 0, pages,
+                                                n_pages, page_size, block_table, table_width, B, T, d, q_pe, qpe_ld_t,
+                                                qpe_ld_h, q, H, d_q, dtype, S(stream), err));
+}
+
+size_t attn_decode_paged_workspace_size(int B, int H, int d_v, int64_t rows_max) {
+  if (B < 1 || H < 1 || d_v < 1 || rows_max < 0) return 0;
+  const int units = paged_units_cc(B, H, rows_max);
+  return round_up(paged_slots(units) * paged_part_block(H, d_v) * sizeof(float), 256);
+}
+
+static csa_status run_paged_attention(PagedAttnArgs& a, int dtype, void* workspace, size_t ws_bytes, void* stream) {
+  REQUIRE(dtype == CSA_F32 || dtype == CSA_BF16, CSA_ERR_DTYPE);
+  csa_status s = paged_checks(a.pages, a.n_pages, a.page, a.table, a.table_w, a.B);
+  if (s != CSA_OK) return s;
+  s = attn_common_checks(a.q, a.pages, a.win, a.sink, a.B, a.H, a.dk, a.dv, 1, a.W, dtype, a.out, a.lse);
+  if (s != CSA_OK) return s;
+  REQUIRE(a.W == 0 || a.win_len, CSA_ERR_NULL);
+  REQUIRE(isfinite(a.sm_scale), CSA_ERR_SHAPE);
+  REQUIRE(workspace && ws_bytes >= attn_decode_paged_workspace_size(a.B, a.H, a.dv, paged_rows_max(a)), CSA_ERR_WORKSPACE);
+  REQUIRE(aligned16(workspace), CSA_ERR_ALIGN);
+  a.part = (float*)workspace;
+  a.err = device_error_word();
+  REQUIRE(a.err, CSA_ERR_CUDA);
+  return cuda_status(launch_paged_attn_cc(a, dtype, S(stream)));
+}
+
+csa_status hca_attn_decode_paged(const void* q, const void* pages, int64_t n_pages, int page_size,
+                                 const int32_t* block_table, int table_width, const int32_t* n_entries, const void* win,
+                                 const int32_t* win_len, const float* sink, int B, int H, int d_k, int d_v, int W,
+                                 float sm_scale, int dtype, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  REQUIRE(n_entries, CSA_ERR_NULL);
+  PagedAttnArgs a{};
+  a.q = q; a.pages = pages; a.n_pages = n_pages; a.page = page_size; a.table = block_table; a.table_w = table_width;
+  a.n_entries = n_entries; a.win = win; a.win_len = win_len; a.W = W; a.sink = sink; a.B = B; a.H = H; a.dk = d_k;
+  a.dv = d_v; a.sm_scale = sm_scale; a.out = out; a.lse = lse;
+  return run_paged_attention(a, dtype, workspace, ws_bytes, stream);
+}
+
+csa_status sparse_attn_decode_paged(const void* q, const void* pages, int64_t n_pages, int page_size,
+                                    const int32_t* block_table, int table_width, const int32_t* idx, int k,
+                                    const void* win, const int32_t* win_len, const float* sink, int B, int H, int d_k,
+                                    int d_v, int W, float sm_scale, int dtype, void* out, float* lse, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+  REQUIRE(idx, CSA_ERR_NULL);
+  REQUIRE(k >= 1 && k <= 65536, CSA_ERR_SHAPE);
+  PagedAttnArgs a{};
+  a.q = q; a.pages = pages; a.n_pages = n_pages; a.page = page_size; a.table = block_table; a.table_w = table_width;
+  a.idx = idx; a.k = k; a.win = win; a.win_len = win_len; a.W = W; a.sink = sink; a.B = B; a.H = H; a.dk = d_k;
+  a.dv = d_v; a.sm_scale = sm_scale; a.out = out; a.lse = lse;
+  return run_paged_attention(a, dtype, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

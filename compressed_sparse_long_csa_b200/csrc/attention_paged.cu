@@ -1,0 +1,283 @@
+// Attention of one new token per sequence over a paged latent cache, CUDA-core path, and
+// the merge of split sequences.
+//
+// For head h of sequence b, over its rows (all entries, or the selected ones, and the
+// window rows):  l_r = s <q_h, row_r>,  out_h = sum_r e^{l_r - M} row_r[0:dv] / den,
+// den = e^{sink_h - M} + sum_r e^{l_r - M}, M = max(sink_h, max_r l_r), lse_h = M + log den.
+// The same attention as sparse_attn_decode / hca_attn_decode ("Техотчёт DeepSeek-V4
+// (2026): миллион токенов контекста", section "Гибридное внимание: CSA и HCA", CSA step 3
+// and the HCA paragraph; sink, window and latent of "Технический отчёт DeepSeek-V4 —
+// часть 1/2"); the page table is the addition.
+//
+// This path takes every shape and both storage types in fp32 arithmetic.
+#include "paged.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int PC_ROWS = 32;      // rows per tile: one lane per row in the logits
+constexpr int PC_WARPS = 8;      // heads per CTA: one warp each
+constexpr int PC_MAXD = 576;
+constexpr int PC_MIN_TILES = 2;
+
+// grid (units, ceil(H / 8)); shared memory [32][dk + 4] rows and [8][dk] queries, fp32.
+// Logits: lane r of a head's warp forms the whole dot product of row r (no reduction
+// across lanes); the pitch dk + 4 spreads the lanes' 16-byte loads over the banks.
+// Values: lane i owns dims 4i .. 4i+3 (+128 j).
+template <typename T>
+__global__ void __launch_bounds__(PC_WARPS * 32)
+paged_attn_cc_kernel(PagedAttnArgs a) {
+  extern __shared__ float4 smem4[];
+  __shared__ int64_t scratch[66];
+  __shared__ int64_t rowi[PC_ROWS];                  // row of the pool, -1 = none
+  const int unit = blockIdx.x, hg = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
+  const int dk = a.dk, dv = a.dv, pitch = dk + 4;
+  float* Ks = reinterpret_cast<float*>(smem4);
+  float* Qs = Ks + PC_ROWS * pitch + (size_t)warp * dk;
+  const int h = hg * PC_WARPS + warp;
+  const bool hv = h < a.H;
+  constexpr int VEC = Elem<T>::VEC;
+  const int vecs = dk / VEC;
+  constexpr int NO = (PC_MAXD + 127) / 128;          // groups of 4 dims per lane
+
+  const PagedPlan plan = paged_plan(a, unit, threads, scratch);
+  // sequences without a row: no unit has a tile of theirs
+  for (int b = unit; b < a.B; b += a.units) {
+    if (paged_tiles(a, b) != 0 || !hv) continue;
+    for (int c = lane; c < dv; c += 32) Elem<T>::st((T*)a.out + ((size_t)b * a.H + h) * dv + c, 0.f);
+    if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
+  }
+  int64_t left = min(plan.per, plan.total - (int64_t)unit * plan.per);
+  int b = plan.b;
+  int64_t t = (int64_t)unit * plan.per - plan.before;
+  for (; left > 0; ++b, t = 0) {
+    const int na = paged_rows_a(a, b), nw = paged_rows_w(a, b);
+    const int64_t ta = ((int64_t)na + PC_ROWS - 1) / PC_ROWS, tiles = ta + (nw + PC_ROWS - 1) / PC_ROWS;
+    if (t >= tiles) continue;
+    const int64_t t1 = min(tiles, t + left);
+    const bool whole = t == 0 && t1 == tiles;
+    const int slot = 2 * unit + (t == 0 ? 1 : 0);
+    left -= t1 - t;
+    if (hv)
+      for (int c = lane * VEC; c < dk; c += 32 * VEC) {
+        float x[VEC];
+        Elem<T>::ld_vec((const T*)a.q + ((size_t)b * a.H + h) * dk + c, x);
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) Qs[c + u] = x[u];
+      }
+    float4 o[NO];
+#pragma unroll
+    for (int i = 0; i < NO; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m_run = -INFINITY, l_run = 0.f;
+    for (; t < t1; ++t) {
+      __syncthreads();                                // the tile before is no longer read
+      const bool in_a = t < ta;
+      const int64_t v0 = (in_a ? t : t - ta) * PC_ROWS;
+      if (threadIdx.x < PC_ROWS) {
+        const int64_t v = v0 + threadIdx.x;
+        rowi[threadIdx.x] = in_a ? (v < na ? paged_row(a, b, (int)v) : -1) : (v < nw ? (int64_t)b * a.W + v : -1);
+      }
+      __syncthreads();
+      const T* base = in_a ? (const T*)a.pages : (const T*)a.win;
+      for (int i = threadIdx.x; i < PC_ROWS * vecs; i += threads) {
+        const int r = i / vecs, c = (i - r * vecs) * VEC;
+        float x[VEC];
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) x[u] = 0.f;
+        if (rowi[r] >= 0) Elem<T>::ld_vec(base + (size_t)rowi[r] * dk + c, x);
+#pragma unroll
+        for (int u = 0; u < VEC; u += 4)
+          *reinterpret_cast<float4*>(Ks + r * pitch + c + u) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+      }
+      __syncthreads();
+      if (!hv) continue;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      const float* kr = Ks + lane * pitch;
+#pragma unroll 4
+      for (int c = 0; c < dk; c += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(kr + c), y = *reinterpret_cast<const float4*>(Qs + c);
+        s0 = fmaf(x.x, y.x, s0);
+        s1 = fmaf(x.y, y.y, s1);
+        s2 = fmaf(x.z, y.z, s2);
+        s3 = fmaf(x.w, y.w, s3);
+      }
+      const float logit = rowi[lane] >= 0 ? ((s0 + s1) + (s2 + s3)) * a.sm_scale : -INFINITY;
+      const float m_new = fmaxf(m_run, warp_max(logit));
+      if (m_new == -INFINITY) continue;               // no row of the piece so far
+      const float alpha = __expf(m_run - m_new);
+      const float p = __expf(logit - m_new);
+      l_run = l_run * alpha + warp_sum(p);
+      m_run = m_new;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) { o[i].x *= alpha; o[i].y *= alpha; o[i].z *= alpha; o[i].w *= alpha; }
+      for (int r = 0; r < PC_ROWS; ++r) {
+        const float pr = __shfl_sync(0xffffffffu, p, r);
+        const float* vr = Ks + r * pitch + 4 * lane;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          if (4 * lane + 128 * i < dv) {
+            const float4 x = *reinterpret_cast<const float4*>(vr + 128 * i);
+            o[i].x = fmaf(pr, x.x, o[i].x);
+            o[i].y = fmaf(pr, x.y, o[i].y);
+            o[i].z = fmaf(pr, x.z, o[i].z);
+            o[i].w = fmaf(pr, x.w, o[i].w);
+          }
+        }
+      }
+    }
+    if (!hv) continue;
+    if (whole) {
+      const float sk = a.sink[h], M = fmaxf(sk, m_run);
+      float den = 0.f, f = 0.f;
+      if (M != -INFINITY) {
+        f = m_run == -INFINITY ? 0.f : __expf(m_run - M);
+        den = __expf(sk - M) + l_run * f;
+      }
+      const float inv = den > 0.f ? f / den : 0.f;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        const int c = 4 * lane + 128 * i;
+        if (c < dv) {
+          T* dst = (T*)a.out + ((size_t)b * a.H + h) * dv + c;
+          Elem<T>::st(dst, o[i].x * inv);
+          Elem<T>::st(dst + 1, o[i].y * inv);
+          Elem<T>::st(dst + 2, o[i].z * inv);
+          Elem<T>::st(dst + 3, o[i].w * inv);
+        }
+      }
+      if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+    } else {
+      float* blk = a.part + (size_t)slot * paged_part_block(a.H, dv);
+#pragma unroll
+      for (int i = 0; i < NO; ++i) {
+        const int c = 4 * lane + 128 * i;
+        if (c < dv) *reinterpret_cast<float4*>(blk + paged_part_val(a.H, h, c)) = o[i];
+      }
+      if (lane == 0) {
+        float* rec = blk + paged_part_rec(a.H, dv, h);
+        rec[0] = m_run;
+        rec[1] = l_run;
+      }
+    }
+  }
+}
+
+// Joins the pieces of cut sequences: out = sum_p e^{m_p - M} o_p / (e^{sink - M} +
+// sum_p e^{m_p - M} l_p).  grid (units, ceil(H / 8)): CTA u takes the sequence that begins in
+// unit u and goes on after it, if there is one, for eight heads.  The pieces are added in
+// order, so a result does not depend on the order in which the units ended.  Thread (h, j)
+// of 8 x 16: eight heads' 16-byte pieces of a partial are one 128-byte line.
+constexpr int PM_H = 8, PM_J = 16;
+template <typename T>
+__global__ void __launch_bounds__(PM_H * PM_J)
+paged_merge_kernel(PagedAttnArgs a) {
+  extern __shared__ float wts[];                     // [piece][8] e^{m_p - M} / den
+  __shared__ int64_t scratch[66];
+  __shared__ float red[4][PM_H];
+  const int unit = blockIdx.x, dv = a.dv, H = a.H;
+  const int hl = threadIdx.x & (PM_H - 1), j = threadIdx.x / PM_H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * PM_H + hl;
+  const bool hv = h < H;
+  const PagedPlan plan = paged_plan(a, unit + 1, PM_H * PM_J, scratch);
+  const int64_t cut = (int64_t)(unit + 1) * plan.per;                  // first tile of the next unit
+  if (plan.b >= a.B || plan.before >= cut || plan.before < cut - plan.per) return;
+  const int b = plan.b;
+  const int n = (int)((plan.before + paged_tiles(a, b) - 1) / plan.per) - unit + 1;
+  // piece p lies in unit `unit + p`: slot 1 where the sequence begins, slot 0 after it
+  auto block = [&](int p) { return a.part + (size_t)(2 * (unit + p) + (p == 0)) * paged_part_block(H, dv); };
+  auto across = [&](float v, bool mx) {              // over the 16 threads of a head
+#pragma unroll
+    for (int o = PM_H; o < 32; o <<= 1) {
+      const float w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = mx ? fmaxf(v, w) : v + w;
+    }
+    __syncthreads();
+    if (lane < PM_H) red[warp][lane] = v;
+    __syncthreads();
+    const float r0 = red[0][hl], r1 = red[1][hl], r2 = red[2][hl], r3 = red[3][hl];
+    return mx ? fmaxf(fmaxf(r0, r1), fmaxf(r2, r3)) : (r0 + r1) + (r2 + r3);
+  };
+  const float sk = hv ? a.sink[h] : -INFINITY;
+  float M = sk;
+  for (int p = j; p < n; p += PM_J) {
+    const float m = hv ? block(p)[paged_part_rec(H, dv, h)] : -INFINITY;
+    wts[p * PM_H + hl] = m;
+    M = fmaxf(M, m);
+  }
+  M = across(M, true);
+  float den = 0.f;
+  for (int p = j; p < n; p += PM_J) {
+    const float m = wts[p * PM_H + hl];
+    const float w = m == -INFINITY ? 0.f : __expf(m - M);
+    if (hv) den += w * block(p)[paged_part_rec(H, dv, h) + 1];
+    wts[p * PM_H + hl] = w;
+  }
+  den = across(den, false) + (sk == -INFINITY ? 0.f : __expf(sk - M));
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  if (!hv) return;
+  for (int c = 4 * j; c < dv; c += 4 * PM_J) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* src = block(0) + paged_part_val(H, h, c);
+    float w = wts[hl];
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+      if (p + 1 < n) {
+        src = block(p + 1) + paged_part_val(H, h, c);
+        w = wts[(p + 1) * PM_H + hl];
+      }
+    }
+    T* dst = (T*)a.out + ((size_t)b * H + h) * dv + c;
+    Elem<T>::st(dst, acc.x * inv);
+    Elem<T>::st(dst + 1, acc.y * inv);
+    Elem<T>::st(dst + 2, acc.z * inv);
+    Elem<T>::st(dst + 3, acc.w * inv);
+  }
+  if (a.lse && j == 0) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
+  const dim3 grid(a.units, (a.H + PM_H - 1) / PM_H);
+  const size_t smem = (size_t)a.units * PM_H * sizeof(float);          // a sequence has at most `units` pieces
+  note_launch();
+  if (dtype == CSA_BF16) paged_merge_kernel<__nv_bfloat16><<<grid, PM_H * PM_J, smem, st>>>(a);
+  else paged_merge_kernel<float><<<grid, PM_H * PM_J, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Two CTAs per SM over the head groups.
+int paged_units_cc(int B, int H, int64_t rows_max) {
+  const int groups = (H + PC_WARPS - 1) / PC_WARPS;
+  return paged_units(2 * num_sms() / groups, B, rows_max, PC_ROWS, PC_MIN_TILES);
+}
+
+cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
+  a.units = paged_units_cc(a.B, a.H, paged_rows_max(a));
+  a.tile = PC_ROWS;
+  a.min_tiles = PC_MIN_TILES;
+  const int warps = a.H < PC_WARPS ? a.H : PC_WARPS;
+  const size_t smem = ((size_t)PC_ROWS * (a.dk + 4) + (size_t)warps * a.dk) * sizeof(float);
+  dim3 grid(a.units, (a.H + PC_WARPS - 1) / PC_WARPS);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_cc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    paged_attn_cc_kernel<T><<<grid, warps * 32, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_paged_merge(a, dtype, st);
+  };
+  return dtype == CSA_BF16 ? go(__nv_bfloat16()) : go(float());
+}
+
+}  // namespace csa

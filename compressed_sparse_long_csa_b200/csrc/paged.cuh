@@ -1,0 +1,150 @@
+// Internal arguments and the work schedule of the paged-cache attention kernels.
+//
+// A paged cache is a pool of pages [n_pages, page, d_k]; entry e of sequence b is row
+// e % page of page table[b, e / page].
+#pragma once
+#include "common.cuh"
+
+namespace csa {
+
+struct PagedAttnArgs {
+  const void* q;              // [B, H, dk]
+  const void* pages;          // [n_pages, page, dk]
+  int64_t n_pages;
+  int page;
+  const int32_t* table;       // [B, table_w] page of each run of `page` entries
+  int table_w;
+  const int32_t* n_entries;   // [B] (dense) or null
+  const int32_t* idx;         // [B, k] (sparse) or null
+  int k;
+  const void* win;            // [B, W, dk]
+  const int32_t* win_len;     // [B]
+  int W;
+  const float* sink;          // [H]
+  int B, H, dk, dv;
+  float sm_scale;
+  void* out;                  // [B, H, dv]
+  float* lse;                 // [B, H] or null
+  float* part;                // partials of split sequences: paged_slots(units) blocks
+  int units;                  // work units (CTAs per head group)
+  int tile;                   // rows per tile of the schedule
+  int min_tiles;              // least tiles of a unit
+  unsigned* err;
+};
+
+// Entries that the table has room for.
+__host__ __device__ inline int64_t paged_capacity(const PagedAttnArgs& a) { return (int64_t)a.table_w * a.page; }
+
+// ---- schedule ---------------------------------------------------------------------------------
+// The rows of a sequence are cut into tiles of `tile` rows: its entries (or index slots)
+// first, then its window rows, so that no tile mixes the two.  The tiles of all sequences,
+// in order, are dealt to the units in equal runs of q tiles: every unit streams the same
+// number of rows however ragged the lengths are, and the lengths are read on the device
+// only.  A sequence whose tiles lie in one unit is finished there; one that is cut leaves a
+// partial (o, m, l) in each unit it touches, and a merge kernel joins them.  A unit holds at
+// most two pieces of cut sequences: one of a sequence that began before it (slot 0) and one
+// of a sequence that goes on after it (slot 1).
+__device__ __forceinline__ int paged_rows_a(const PagedAttnArgs& a, int b) {
+  if (a.idx) return a.k;
+  const int64_t n = a.n_entries[b], cap = paged_capacity(a);
+  return (int)(n < 0 ? 0 : (n > cap ? cap : n));
+}
+__device__ __forceinline__ int paged_rows_w(const PagedAttnArgs& a, int b) {
+  if (a.W == 0) return 0;
+  const int n = a.win_len[b];
+  return n < 0 ? 0 : (n > a.W ? a.W : n);
+}
+__device__ __forceinline__ int64_t paged_tiles(const PagedAttnArgs& a, int b) {
+  return ((int64_t)paged_rows_a(a, b) + a.tile - 1) / a.tile + (paged_rows_w(a, b) + a.tile - 1) / a.tile;
+}
+
+struct PagedPlan {
+  int64_t total;     // tiles of all sequences
+  int64_t per;       // tiles of a unit
+  int64_t before;    // tiles of the sequences before sequence b
+  int b;             // the sequence that holds tile `at` (B when there is none)
+};
+
+// The plan, and the sequence that holds tile unit * per.  All `threads` threads of the block
+// call it; scratch: 66 int64 in shared memory.
+__device__ __forceinline__ PagedPlan paged_plan(const PagedAttnArgs& a, int unit, int threads, int64_t* scratch) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
+  const int chunk = (a.B + threads - 1) / threads;
+  const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += paged_tiles(a, b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  if (tid == 0) { scratch[64] = 0; scratch[65] = a.B; }
+  __syncthreads();
+  int64_t at = incl - mine, total = 0;                // tiles before this thread's sequences, and all
+  for (int w = 0; w < warps; ++w) {
+    const int64_t v = scratch[w];
+    if (w < warp) at += v;
+    total += v;
+  }
+  int64_t per = (total + a.units - 1) / a.units;
+  if (per < a.min_tiles) per = a.min_tiles;
+  const int64_t first = (int64_t)unit * per;
+  if (first >= at && first < at + mine) {             // one thread at most
+    int b = b0;
+    for (;; ++b) {
+      const int64_t n = paged_tiles(a, b);
+      if (first < at + n) break;
+      at += n;
+    }
+    scratch[64] = at;
+    scratch[65] = b;
+  }
+  __syncthreads();
+  PagedPlan p;
+  p.total = total;
+  p.per = per;
+  p.before = scratch[64];
+  p.b = (int)scratch[65];
+  return p;
+}
+
+// Floats of one partial: o as [dv / 4][H][4] (consecutive heads store contiguous 16-byte
+// pieces), then [H][4] records {m, l, -, -}.  m and l belong to natural-log logits.
+__host__ __device__ inline size_t paged_part_block(int H, int dv) { return (size_t)H * (dv + 4); }
+__host__ __device__ inline size_t paged_part_val(int H, int h, int c) { return ((size_t)(c >> 2) * H + h) * 4 + (c & 3); }
+__host__ __device__ inline size_t paged_part_rec(int H, int dv, int h) { return (size_t)dv * H + 4 * (size_t)h; }
+
+// Row v of segment A (entries or index slots) of sequence b: its row in the pool, or -1
+// (an unused slot, or a bad entry or page, which sets CSA_DEVERR_INDEX).
+__device__ __forceinline__ int64_t paged_row(const PagedAttnArgs& a, int b, int v) {
+  int e = v;
+  if (a.idx) {
+    e = a.idx[(size_t)b * a.k + v];
+    if (e < 0) return -1;
+    if ((int64_t)e >= paged_capacity(a)) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
+  }
+  const unsigned pg = (unsigned)e / (unsigned)a.page;
+  const int id = a.table[(size_t)b * a.table_w + pg];
+  if (id < 0 || (int64_t)id >= a.n_pages) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
+  return (int64_t)id * a.page + (e - (int)pg * a.page);
+}
+
+// Units of an attention launch over `ctas` CTAs per head group: no more than the tiles that
+// the shapes allow, so that a short context launches few CTAs.
+inline int paged_units(int ctas, int B, int64_t rows_max, int tile, int min_tiles) {
+  const int64_t tiles = (int64_t)B * (rows_max / tile + 2);            // entries and window end in their own tiles
+  const int64_t u = (tiles + min_tiles - 1) / min_tiles;
+  return (int)(u < ctas ? (u < 1 ? 1 : u) : (ctas < 1 ? 1 : ctas));
+}
+inline size_t paged_slots(int units) { return 2 * (size_t)units; }
+// Rows that one sequence may have: the workspace size and the launch use the same number.
+inline int64_t paged_rows_max(const PagedAttnArgs& a) { return (a.idx ? (int64_t)a.k : paged_capacity(a)) + a.W; }
+int paged_units_cc(int B, int H, int64_t rows_max);
+
+// Joins the pieces of cut sequences (a.units, a.tile and a.min_tiles as in the attention launch).
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st);
+cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st);
+
+}  // namespace csa

@@ -499,6 +499,77 @@ csa_status sparse_attn_decode_noalloc(const void* q, const void* cache, const in
                                       int B, int H, int d_k, int d_v, int64_t n_max, int k, int W,
                                       float sm_scale, int dtype, void* out, float* lse, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged caches.  A paged cache is a pool of pages [n_pages, page_size, d]; entry e of
+ * sequence b is row e % page_size of page block_table[b, e / page_size].  Sequences share
+ * the pool, so a cache grows a page at a time and its pages may lie anywhere in it.  The
+ * pages of the report give the rows and the attention, not their paging.
+ *   pages        device [n_pages, page_size, d] dtype
+ *   block_table  device [B, table_width] int32 page ids; ids past a sequence's last entry
+ *                are never read
+ * Supported: page_size 1 .. 65536 (any value; the tensor-core attention copies pages of
+ * 8 rows and more by TMA when their size shares a factor of 8, 16, 32 or 64 with 64),
+ * table_width * page_size and n_pages * page_size < 2^31.
+ *
+ * latent_append_paged — the cache append of T new rows, with the position rotation applied
+ * on the way ("Технический отчёт DeepSeek-V4 — часть 1/2": the latent's last 64 of 576
+ * dims carry the position), and the same rotation of the queries' rotary parts into the
+ * query rows that the attention reads.
+ *   rows     device [T] rows of d values, rows_ld elements apart (a slice of a wider
+ *            projection, or rows_ld = d): row t goes to entry entry[t] of sequence seq[t],
+ *            its last d_r values rotated
+ *   seq      device [T] int32, or NULL: row t belongs to sequence t (T <= B)
+ *   entry    device [T] int32; a negative entry marks a padding row: nothing of the token is
+ *            read or written
+ *   pos      device [T] int32 rotation positions, or NULL: the position is entry[t]
+ *   inv_freq device [d_r / 2] fp32 frequencies (radians per position), or NULL with
+ *            d_r = 0: no rotation.  The angle pos * inv_freq is formed in fp64.
+ *   interleaved  nonzero: pair i is values (2i, 2i + 1); 0: (i, i + d_r / 2)
+ *   q_pe     device: head h of token t at q_pe + t * qpe_ld_t + h * qpe_ld_h (elements), d_r
+ *            values; may be the last d_r values of q's own rows (rotated in place)
+ *   q        device [T, H, d_q] dtype, or NULL (no queries): the last d_r values of each row
+ *            are written, the others left alone
+ * A token whose sequence or entry is out of range, or whose page id is outside
+ * [0, n_pages), is skipped whole and sets CSA_DEVERR_ENTRY.  The entries of one call must
+ * differ: of two rows for one entry, either may be stored, or parts of both.
+ * Arithmetic is fp32, rounded once to dtype (a row without rotation is copied bit for bit).
+ * Supported: d <= 576; d, d_r, d_q, rows_ld, qpe_ld_t and qpe_ld_h multiples of 8 (bf16) or
+ * 4 (f32), d_r of twice that when not interleaved; H <= 128.
+ *
+ * hca_attn_decode_paged / sparse_attn_decode_paged — hca_attn_decode and
+ * sparse_attn_decode over a paged cache.
+ *   n_entries device [B] int32: entries 0 .. n_entries[b] - 1 are attended (clamped to
+ *            [0, table_width * page_size])
+ *   idx      device [B, k] int32 entry ids (-1 = unused slot)
+ *   other arguments, and the results, as in those calls; a sequence without entries and
+ *   window rows gives out = 0 and lse = sink.  Rows whose entry or page id is out of range
+ *   are skipped and set CSA_DEVERR_INDEX.  Values of rows that are not attended (the rest of
+ *   a sequence's last page, unused window rows) have no effect, whatever they hold.
+ *   workspace >= attn_decode_paged_workspace_size(B, H, d_v, rows_max) bytes with rows_max =
+ *   table_width * page_size + W (dense) or k + W (sparse).  Its contents need not be kept or
+ *   cleared between calls; calls that may overlap on the GPU need workspaces of their own.
+ * The work of a call follows the lengths found on the device, not the table's width, and
+ * is dealt evenly over the SMs however ragged the lengths are.
+ * Supported: H <= 128, d_v <= d_k <= 576, d_k % 8 == 0, d_v % 4 == 0, W <= 4096, k <= 65536.
+ * ------------------------------------------------------------------------- */
+csa_status latent_append_paged(const void* rows, int64_t rows_ld, const int32_t* seq, const int32_t* entry,
+                               const int32_t* pos, const float* inv_freq, int d_r, int interleaved,
+                               void* pages, int64_t n_pages, int page_size,
+                               const int32_t* block_table, int table_width, int B, int T, int d,
+                               const void* q_pe, int64_t qpe_ld_t, int64_t qpe_ld_h, void* q, int H, int d_q,
+                               int dtype, void* stream);
+size_t attn_decode_paged_workspace_size(int B, int H, int d_v, int64_t rows_max);
+csa_status hca_attn_decode_paged(const void* q, const void* pages, int64_t n_pages, int page_size,
+                                 const int32_t* block_table, int table_width, const int32_t* n_entries,
+                                 const void* win, const int32_t* win_len, const float* sink,
+                                 int B, int H, int d_k, int d_v, int W, float sm_scale, int dtype,
+                                 void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+csa_status sparse_attn_decode_paged(const void* q, const void* pages, int64_t n_pages, int page_size,
+                                    const int32_t* block_table, int table_width, const int32_t* idx, int k,
+                                    const void* win, const int32_t* win_len, const float* sink,
+                                    int B, int H, int d_k, int d_v, int W, float sm_scale, int dtype,
+                                    void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
