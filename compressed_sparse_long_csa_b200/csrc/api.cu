@@ -739,8 +739,8 @@ csa_status latent_append_paged(const void* rows, int64_t rows_ld, const int32_t*
 
 size_t attn_decode_paged_workspace_size(int B, int H, int d_v, int64_t rows_max) {
   if (B < 1 || H < 1 || d_v < 1 || rows_max < 0) return 0;
-  const int units = paged_units_cc(B, H, rows_max);
-  return round_up(paged_slots(units) * paged_part_block(H, d_v) * sizeof(float), 256);
+  const int cc = paged_units_cc(B, H, rows_max), tc = paged_units_tc(B, H, rows_max);
+  return round_up(paged_slots(cc > tc ? cc : tc) * paged_part_block(H, d_v) * sizeof(float), 256);
 }
 
 static csa_status run_paged_attention(PagedAttnArgs& a, int dtype, void* workspace, size_t ws_bytes, void* stream) {
@@ -756,6 +756,7 @@ static csa_status run_paged_attention(PagedAttnArgs& a, int dtype, void* workspa
   a.part = (float*)workspace;
   a.err = device_error_word();
   REQUIRE(a.err, CSA_ERR_CUDA);
+  if (tc_enabled() && dtype == CSA_BF16 && a.dk == 576 && a.dv == 512) return cuda_status(launch_paged_attn_tc(a, S(stream)));
   return cuda_status(launch_paged_attn_cc(a, dtype, S(stream)));
 }
 

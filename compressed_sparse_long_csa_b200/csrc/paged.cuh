@@ -142,9 +142,12 @@ inline size_t paged_slots(int units) { return 2 * (size_t)units; }
 // Rows that one sequence may have: the workspace size and the launch use the same number.
 inline int64_t paged_rows_max(const PagedAttnArgs& a) { return (a.idx ? (int64_t)a.k : paged_capacity(a)) + a.W; }
 int paged_units_cc(int B, int H, int64_t rows_max);
+int paged_units_tc(int B, int H, int64_t rows_max);
 
 // Joins the pieces of cut sequences (a.units, a.tile and a.min_tiles as in the attention launch).
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st);
+// bf16, d_k = 576, d_v = 512 only.
+cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st);
 
 }  // namespace csa

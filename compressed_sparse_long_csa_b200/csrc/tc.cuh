@@ -121,6 +121,18 @@ __device__ __forceinline__ void mma_f16_c(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACC ? 1 : 0) : "memory");
 }
+// kind::f16 in the weight-stationary form (.ws) at M = 64: the accumulator takes 64 lanes x
+// N / 2 columns twice (lanes 0-63 columns 0 .. N/2-1 of D, lanes 64-127 the other half), so
+// it uses every TMEM lane, and an MMA of N = 256 takes 80 cycles where the plain form's
+// accumulator (16 lanes of each 32) takes 128; N = 64: 32 cycles either way (both bound by
+// the 128 bytes per cycle of shared memory that A and B come from).
+template <bool ACC>
+__device__ __forceinline__ void mma_f16_ws(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACC ? 1 : 0) : "memory");
+}
 // One lane of a converged warp (the same lane every time the whole warp calls it).  MMAs
 // are issued as `if (elect_one()) mma(...)` by a converged warp whose lanes all compute the
 // (warp-uniform) descriptors: the issue then keeps pace with N = 64 MMAs, where a lone
