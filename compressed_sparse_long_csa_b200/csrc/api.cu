@@ -740,7 +740,7 @@ csa_status latent_append_paged(const void* rows, int64_t rows_ld, const int32_t*
 size_t attn_decode_paged_workspace_size(int B, int H, int d_v, int64_t rows_max) {
   if (B < 1 || H < 1 || d_v < 1 || rows_max < 0) return 0;
   const int cc = paged_units_cc(B, H, rows_max), tc = paged_units_tc(B, H, rows_max);
-  return round_up(paged_slots(cc > tc ? cc : tc) * paged_part_block(H, d_v) * sizeof(float), 256);
+  return round_up(paged_ws_bytes(cc > tc ? cc : tc, H, d_v), 256);
 }
 
 static csa_status run_paged_attention(PagedAttnArgs& a, int dtype, void* workspace, size_t ws_bytes, void* stream) {

@@ -42,6 +42,7 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
   const int vecs = dk / VEC;
   constexpr int NO = (PC_MAXD + 127) / 128;          // groups of 4 dims per lane
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // the merge waits for this grid itself
   const PagedPlan plan = paged_plan(a, unit, threads, scratch);
   // sequences without a row: no unit has a tile of theirs
   for (int b = unit; b < a.B; b += a.units) {
@@ -49,6 +50,7 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
     for (int c = lane; c < dv; c += 32) Elem<T>::st((T*)a.out + ((size_t)b * a.H + h) * dv + c, 0.f);
     if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
   }
+  if (hg == 0 && threadIdx.x == 0) paged_note(a, plan, unit);
   int64_t left = min(plan.per, plan.total - (int64_t)unit * plan.per);
   int b = plan.b;
   int64_t t = (int64_t)unit * plan.per - plan.before;
@@ -165,93 +167,120 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
 }
 
 // Joins the pieces of cut sequences: out = sum_p e^{m_p - M} o_p / (e^{sink - M} +
-// sum_p e^{m_p - M} l_p).  grid (units, ceil(H / 8)): CTA u takes the sequence that begins in
-// unit u and goes on after it, if there is one, for eight heads.  The pieces are added in
-// order, so a result does not depend on the order in which the units ended.  Thread (h, j)
-// of 8 x 16: eight heads' 16-byte pieces of a partial are one 128-byte line.
-constexpr int PM_H = 8, PM_J = 16;
+// sum_p e^{m_p - M} l_p).  The units noted which sequences they began and did not finish;
+// every CTA gathers those notes and takes its share of the items (sequence, eight heads,
+// slice of the dims), the slices as narrow as it takes to give every CTA an item.  Thread
+// (head, 16-byte piece of dims): eight heads' pieces of a partial are one 128-byte line.
+// The pieces are added in order, so a result does not depend on the order in which the
+// units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece.
+constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 8;
 template <typename T>
-__global__ void __launch_bounds__(PM_H * PM_J)
+__global__ void __launch_bounds__(PM_THREADS)
 paged_merge_kernel(PagedAttnArgs a) {
-  extern __shared__ float wts[];                     // [piece][8] e^{m_p - M} / den
-  __shared__ int64_t scratch[66];
-  __shared__ float red[4][PM_H];
-  const int unit = blockIdx.x, dv = a.dv, H = a.H;
+  extern __shared__ float wts[];                     // [units][8] e^{m_p - M} / den, then the list
+  __shared__ float red[PM_THREADS / 32][PM_H];
+  __shared__ int count;
+  int* list = reinterpret_cast<int*>(wts + (size_t)a.units * PM_H);
+  const int dv = a.dv, H = a.H;
   const int hl = threadIdx.x & (PM_H - 1), j = threadIdx.x / PM_H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * PM_H + hl;
-  const bool hv = h < H;
-  const PagedPlan plan = paged_plan(a, unit + 1, PM_H * PM_J, scratch);
-  const int64_t cut = (int64_t)(unit + 1) * plan.per;                  // first tile of the next unit
-  if (plan.b >= a.B || plan.before >= cut || plan.before < cut - plan.per) return;
-  const int b = plan.b;
-  const int n = (int)((plan.before + paged_tiles(a, b) - 1) / plan.per) - unit + 1;
-  // piece p lies in unit `unit + p`: slot 1 where the sequence begins, slot 0 after it
-  auto block = [&](int p) { return a.part + (size_t)(2 * (unit + p) + (p == 0)) * paged_part_block(H, dv); };
-  auto across = [&](float v, bool mx) {              // over the 16 threads of a head
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2* notes = paged_notes(a);
+  if (warp == 0) {
+    int n = 0;
+    for (int u0 = 0; u0 < a.units; u0 += 32) {
+      const bool cut = u0 + lane < a.units && __ldcg(&notes[u0 + lane]).y > 0;
+      const unsigned m = __ballot_sync(0xffffffffu, cut);
+      if (cut) list[n + __popc(m & ((1u << lane) - 1u))] = u0 + lane;
+      n += __popc(m);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int hb = (H + PM_H - 1) / PM_H, c4 = dv / 4;
+  int slices = 1;
+  while (slices < PM_SLICES && count * hb * slices < (int)gridDim.x) slices <<= 1;
+  const int width = (c4 + slices - 1) / slices;       // 16-byte pieces of a slice
+  for (int item = blockIdx.x; item < count * hb * slices; item += gridDim.x) {
+    const int sl = item % slices, blk8 = item / slices % hb, unit = list[item / (slices * hb)];
+    const int2 note = __ldcg(&notes[unit]);
+    const int b = note.x, n = note.y, h = blk8 * PM_H + hl;
+    const bool hv = h < H;
+    // piece 0 lies in slot 1 of the unit, piece p > 0 in slot 0 of unit + p
+    const size_t block = paged_part_block(H, dv);
+    const float* first = a.part + (size_t)(2 * unit + 1) * block;
+    const float* rest = a.part + (size_t)(2 * unit) * block;                // + 2 p blocks
+    auto across = [&](float v, bool mx) {             // over the threads of a head
 #pragma unroll
-    for (int o = PM_H; o < 32; o <<= 1) {
-      const float w = __shfl_xor_sync(0xffffffffu, v, o);
-      v = mx ? fmaxf(v, w) : v + w;
-    }
-    __syncthreads();
-    if (lane < PM_H) red[warp][lane] = v;
-    __syncthreads();
-    const float r0 = red[0][hl], r1 = red[1][hl], r2 = red[2][hl], r3 = red[3][hl];
-    return mx ? fmaxf(fmaxf(r0, r1), fmaxf(r2, r3)) : (r0 + r1) + (r2 + r3);
-  };
-  const float sk = hv ? a.sink[h] : -INFINITY;
-  float M = sk;
-  for (int p = j; p < n; p += PM_J) {
-    const float m = hv ? block(p)[paged_part_rec(H, dv, h)] : -INFINITY;
-    wts[p * PM_H + hl] = m;
-    M = fmaxf(M, m);
-  }
-  M = across(M, true);
-  float den = 0.f;
-  for (int p = j; p < n; p += PM_J) {
-    const float m = wts[p * PM_H + hl];
-    const float w = m == -INFINITY ? 0.f : __expf(m - M);
-    if (hv) den += w * block(p)[paged_part_rec(H, dv, h) + 1];
-    wts[p * PM_H + hl] = w;
-  }
-  den = across(den, false) + (sk == -INFINITY ? 0.f : __expf(sk - M));
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  if (!hv) return;
-  for (int c = 4 * j; c < dv; c += 4 * PM_J) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* src = block(0) + paged_part_val(H, h, c);
-    float w = wts[hl];
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
-      if (p + 1 < n) {
-        src = block(p + 1) + paged_part_val(H, h, c);
-        w = wts[(p + 1) * PM_H + hl];
+      for (int o = PM_H; o < 32; o <<= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = mx ? fmaxf(v, w) : v + w;
       }
+      __syncthreads();
+      if (lane < PM_H) red[warp][lane] = v;
+      __syncthreads();
+      float r = red[0][hl];
+#pragma unroll
+      for (int w = 1; w < PM_THREADS / 32; ++w) r = mx ? fmaxf(r, red[w][hl]) : r + red[w][hl];
+      return r;
+    };
+    const float sk = hv ? a.sink[h] : -INFINITY;
+    float M = sk;
+    const size_t rec = paged_part_rec(H, dv, hv ? h : 0);
+    for (int p = j; p < n; p += PM_C) M = fmaxf(M, __ldcg((p ? rest + 2 * p * block : first) + rec));
+    M = across(M, true);
+    float den = 0.f;
+    for (int p = j; p < n; p += PM_C) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>((p ? rest + 2 * p * block : first) + rec));
+      const float w = ml.x == -INFINITY ? 0.f : __expf(ml.x - M);
+      den += w * ml.y;
+      wts[p * PM_H + hl] = w;
     }
-    T* dst = (T*)a.out + ((size_t)b * H + h) * dv + c;
-    Elem<T>::st(dst, acc.x * inv);
-    Elem<T>::st(dst + 1, acc.y * inv);
-    Elem<T>::st(dst + 2, acc.z * inv);
-    Elem<T>::st(dst + 3, acc.w * inv);
+    den = across(den, false) + (sk == -INFINITY ? 0.f : __expf(sk - M));
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    for (int c = sl * width + j; c < min(c4, (sl + 1) * width) && hv; c += PM_C) {
+      const size_t at = paged_part_val(H, h, 4 * c);
+      float4 x = __ldcg(reinterpret_cast<const float4*>(first + at));
+      float w = wts[hl];
+      float4 acc = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
+#pragma unroll 8
+      for (int p = 1; p < n; ++p) {
+        x = __ldcg(reinterpret_cast<const float4*>(rest + 2 * p * block + at));
+        w = wts[p * PM_H + hl];
+        acc.x = fmaf(w, x.x, acc.x);
+        acc.y = fmaf(w, x.y, acc.y);
+        acc.z = fmaf(w, x.z, acc.z);
+        acc.w = fmaf(w, x.w, acc.w);
+      }
+      T* dst = (T*)a.out + ((size_t)b * H + h) * dv + 4 * c;
+      Elem<T>::st(dst, acc.x * inv);
+      Elem<T>::st(dst + 1, acc.y * inv);
+      Elem<T>::st(dst + 2, acc.z * inv);
+      Elem<T>::st(dst + 3, acc.w * inv);
+    }
+    if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
   }
-  if (a.lse && j == 0) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
 }
 
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
-  const dim3 grid(a.units, (a.H + PM_H - 1) / PM_H);
-  const size_t smem = (size_t)a.units * PM_H * sizeof(float);          // a sequence has at most `units` pieces
+  if (a.units == 1) return cudaSuccess;                // nothing is ever cut
+  const int64_t most = (int64_t)(a.units - 1) * ((a.H + PM_H - 1) / PM_H) * PM_SLICES;
+  const int grid = 2 * num_sms();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < grid ? most : grid));
+  cfg.blockDim = dim3(PM_THREADS);
+  cfg.dynamicSmemBytes = (size_t)a.units * (PM_H * sizeof(float) + sizeof(int));   // a sequence has at most `units` pieces
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the pieces first of all
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   note_launch();
-  if (dtype == CSA_BF16) paged_merge_kernel<__nv_bfloat16><<<grid, PM_H * PM_J, smem, st>>>(a);
-  else paged_merge_kernel<float><<<grid, PM_H * PM_J, smem, st>>>(a);
-  return cudaGetLastError();
+  return dtype == CSA_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, a)
+                           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, a);
 }
 
 // Two CTAs per SM over the head groups.
@@ -261,9 +290,9 @@ int paged_units_cc(int B, int H, int64_t rows_max) {
 }
 
 cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
-  a.units = paged_units_cc(a.B, a.H, paged_rows_max(a));
   a.tile = PC_ROWS;
   a.min_tiles = PC_MIN_TILES;
+  a.units = paged_units(a, paged_units_cc(a.B, a.H, paged_rows_max(a)));
   const int warps = a.H < PC_WARPS ? a.H : PC_WARPS;
   const size_t smem = ((size_t)PC_ROWS * (a.dk + 4) + (size_t)warps * a.dk) * sizeof(float);
   dim3 grid(a.units, (a.H + PC_WARPS - 1) / PC_WARPS);

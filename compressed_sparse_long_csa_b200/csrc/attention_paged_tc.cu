@@ -8,7 +8,7 @@
 //      swizzle atoms: runs of pages as TMA boxes of gcd(page, 64) rows, other rows (selected
 //      entries, partial tiles, pages that share no factor of 8 with 64) as 16-byte cp.async
 //      with the absent rows zeroed (P = 0 there, and 0 * NaN must not reach the sums);
-//   2. the MMA warp issues S = Q K^T (N = 64, 36 steps of K = 16) into TMEM;
+//   2. one warp issues S = Q K^T (N = 64, 36 steps of K = 16) into TMEM;
 //   3. eight softmax warps read S, agree on the running maximum and write P to shared memory
 //      as two bf16 parts, P_hi = bf16(P) and P_lo = bf16(P - P_hi) (the second into the
 //      tile's rotary atom, which only S reads): P is held to 2^-17, where bf16 alone would
@@ -30,11 +30,11 @@ namespace {
 constexpr int PT_ROWS = 64;              // rows per tile (N of QK^T, K of PV)
 constexpr int PT_HC = 64;                // heads per CTA (MMA M)
 constexpr int PT_ATOMS = 9;              // 576 dims = 9 atoms of 64 dims (128 bytes)
-constexpr int PT_CHUNKS = PT_ATOMS * 8;  // 16-byte chunks per row
+constexpr int PT_LO = 4;                 // atoms of a tile's first half (dims 0-255)
 constexpr int PT_GROUP = 96;             // threads per loader group; group g fills stage g
 constexpr int PT_SMW = 8;                // softmax warps: two warpgroups, one per half of a lane's columns
-constexpr int PT_MMAW = 8;               // the MMA warp
-constexpr int PT_QW = 9;                 // the query warp
+constexpr int PT_SW = 8;                 // the warp of the queries and S
+constexpr int PT_PVW = 9;                // the warp of PV
 constexpr int PT_LDW = 10;               // first loader warp
 constexpr int PT_THREADS = PT_LDW * 32 + 2 * PT_GROUP;
 constexpr int PT_MIN_TILES = 2;
@@ -49,10 +49,11 @@ struct PtSmem {
   uint8_t p[PT_HC * 128];                    // P_hi: 64 heads x 64 rows bf16; between segments the row sums
   float smax[2][2][128];                     // per tile parity and warpgroup: the lanes' tile maxima
   int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
-  uint32_t vmask[2][2];                      // per stage: bit j of word j / 32 set when row j is valid
-  uint64_t full[2], empty[2], sfull[2], sfree[2];
-  uint64_t pfull, pdone, qfull, qfree, ofree, drain;
-  uint64_t pairb[4], segb;                   // softmax warps: the two of the same heads; all eight
+  uint32_t vmask[2][2][2];                   // per stage and use parity: bit j of word j / 32: row j is valid
+  uint64_t full[2][2], empty[2][2];          // per stage and half of the dims (0-255, 256-575)
+  uint64_t sfull[2];
+  uint64_t pfull, pdone, qfull, qfree, ofree, drain[2];
+  uint64_t headb[2], segb;                   // softmax warps: the four of the same heads; all eight
   uint32_t tmem_base;
   int abort_flag;
   int ld_stop[2];                            // per loader group: 1 + the step at which it stops (0 = running)
@@ -133,10 +134,12 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&sm.full[s], PT_GROUP);
-      tc::mbar_init(&sm.empty[s], 1);
+      for (int x = 0; x < 2; ++x) {
+        tc::mbar_init(&sm.full[s][x], 1);
+        tc::mbar_init(&sm.empty[s][x], 1);
+      }
       tc::mbar_init(&sm.sfull[s], 1);
-      tc::mbar_init(&sm.sfree[s], PT_SMW);
+      tc::mbar_init(&sm.drain[s], 1);
       sm.ld_stop[s] = 0;
     }
     tc::mbar_init(&sm.pfull, PT_SMW);
@@ -144,13 +147,12 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     tc::mbar_init(&sm.qfull, 1);
     tc::mbar_init(&sm.qfree, 1);
     tc::mbar_init(&sm.ofree, PT_SMW);
-    tc::mbar_init(&sm.drain, 1);
-    for (int s = 0; s < 4; ++s) tc::mbar_init(&sm.pairb[s], 2);
+    for (int s = 0; s < 2; ++s) tc::mbar_init(&sm.headb[s], 4);
     tc::mbar_init(&sm.segb, PT_SMW);
     sm.abort_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == PT_MMAW) { tc::tmem_alloc(&sm.tmem_base, TM_COLS); tc::tmem_relinquish(); }
+  if (warp == PT_SW) { tc::tmem_alloc(&sm.tmem_base, TM_COLS); tc::tmem_relinquish(); }
   tc::griddep_wait();                               // the setup overlaps the preceding kernel's tail
   tc::fence_before_sync();
   const PagedPlan plan = paged_plan(a, unit, PT_THREADS, reinterpret_cast<int64_t*>(sm.q));
@@ -160,6 +162,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   const uint32_t tmem = sm.tmem_base;
   SegIter seg;
   seg.start(plan, unit);
+  tc::griddep_launch_dependents();                  // the merge waits for this grid itself
 
   if (warp >= PT_LDW) {
     // ------------------------------------------------------------------ loader group g (96 threads)
@@ -193,205 +196,210 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         }
       }
     };
+    // Brings the next tile's rows into the L2 while its stage is still in use.  By plain
+    // prefetches: the copy engine takes about as long for a prefetch as for the copy.
+    auto prefetch = [&]() {
+      if (lg >= PT_ROWS || y < 0) return;
+      const uint8_t* r = reinterpret_cast<const uint8_t*>(in_a ? a.pages : a.win) + (size_t)y * (576 * 2);
+#pragma unroll
+      for (int k = 0; k < PT_ATOMS; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * k));
+    };
     step(g);
-    if (more) resolve();
-    int issued = 0;                                   // tiles this group started (for the drain)
+    if (more) { resolve(); if (g > 0) prefetch(); }
+    int n_lo = 0, n_hi = 0;                           // halves this group started (for the drain)
     for (int i = 0; more; ++i) {
-      const bool go = tc::mbar_wait(&sm.empty[g], (i & 1) ^ 1) && !*(volatile int*)&sm.abort_flag;
-      if (!go) sm.ld_stop[g] = i + 1;                 // the group leaves together at this step's barrier
+      // what needs no free stage comes first: the rows, which of them exist, how they are copied
+      if (*(volatile int*)&sm.abort_flag) sm.ld_stop[g] = i + 1;      // the group leaves together below
       if (lg < PT_ROWS) {
-        sm.rowy[g][lg] = y;
+        sm.rowy[g][lg] = y;                           // (the group's copies of the tile before are issued)
         const uint32_t vb = __ballot_sync(0xffffffffu, y >= 0);
-        if ((lg & 31) == 0) sm.vmask[g][lg >> 5] = vb;
+        if ((lg & 31) == 0) sm.vmask[g][i & 1][lg >> 5] = vb;
       }
       const bool a_tile = in_a;
       named_bar(1 + g, PT_GROUP);
       const int stop = *(volatile int*)&sm.ld_stop[g];
       if (stop != 0 && stop <= i + 1) break;
-      const bool all = (sm.vmask[g][0] & sm.vmask[g][1]) == 0xffffffffu;
+      const bool all = (sm.vmask[g][i & 1][0] & sm.vmask[g][i & 1][1]) == 0xffffffffu;
       const int rows = a_tile ? box : PT_ROWS;        // rows per TMA box; box 0: pages that no box fits
       const bool tma = all && (a_tile ? !SPARSE && box > 0 : true);
+      const uint32_t ph = (i & 1) ^ 1;
+      bool in_time = true;
+      // dims 0-255 as soon as the PV of the stage's last tile is past them, then the rest
       if (tma) {
-        if (lg < PT_ROWS / rows) {
-          if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[g], PT_ATOMS * ATOM);
+        // the first thread of each box
+        if (lg < PT_ROWS && lg % rows == 0) {
           const CUtensorMap* m = a_tile ? &maps.pages : &maps.win;
-          const int y0 = sm.rowy[g][lg * rows];
-          for (int at = 0; at < PT_ATOMS; ++at) tc::tma_load_2d(sm.kv[g][at] + lg * rows * 128, m, &sm.full[g], 64 * at, y0);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
+            in_time = in_time && tc::mbar_wait(&sm.empty[g][x], ph);
+            if (!in_time) break;
+            if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[g][x], (at1 - at0) * ATOM);
+            for (int at = at0; at < at1; ++at)
+              tc::tma_load_2d(sm.kv[g][at] + lg * 128, m, &sm.full[g][x], 64 * at, y);
+            if (x) ++n_hi; else ++n_lo;
+          }
         }
-        if (lg != 0) tc::mbar_arrive(&sm.full[g]);
+        __syncwarp();
       } else {
         const uint8_t* base = reinterpret_cast<const uint8_t*>(a_tile ? a.pages : a.win);
         const uint32_t kv0 = tc::smem_u32(sm.kv[g][0]);
-        int j = lg >= PT_CHUNKS ? 1 : 0, c = lg - j * PT_CHUNKS;
-        for (int p = 0; p < PT_ROWS * PT_CHUNKS / PT_GROUP; ++p) {
-          const int yr = sm.rowy[g][j];
-          cp_async16(kv0 + (c >> 3) * ATOM + sw128_off(j, c & 7), base + (size_t)(yr < 0 ? 0 : yr) * (576 * 2) + c * 16,
-                     yr < 0 ? 0 : 16);
-          c += PT_GROUP - PT_CHUNKS;
-          j += 1;
-          if (c >= PT_CHUNKS) { c -= PT_CHUNKS; j += 1; }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
+          in_time = tc::mbar_wait(&sm.empty[g][x], ph) && in_time;
+          const int n = (at1 - at0) * 8;              // 16-byte chunks of a row's half
+          int j = lg / n, c = lg - j * n;
+          const int dj = PT_GROUP / n, dc = PT_GROUP - dj * n;
+          while (j < PT_ROWS) {
+            const int yr = sm.rowy[g][j], ch = at0 * 8 + c;
+            cp_async16(kv0 + (ch >> 3) * ATOM + sw128_off(j, ch & 7), base + (size_t)(yr < 0 ? 0 : yr) * (576 * 2) + ch * 16,
+                       yr < 0 ? 0 : 16);
+            c += dc;
+            j += dj;
+            if (c >= n) { c -= n; j += 1; }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        ++n_lo;
+        ++n_hi;
       }
-      ++issued;
+      if (!in_time) atomicExch(&sm.abort_flag, 1);
       // resolve the group's next tile while the copies are in flight
       step(2);
-      if (more) resolve();
+      if (more) { resolve(); prefetch(); }
       if (!tma) {
-        cp_async_wait_all();
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         tc::fence_proxy_async_smem();
-        tc::mbar_arrive(&sm.full[g]);
+        named_bar(1 + g, PT_GROUP);
+        if (lg == 0) tc::mbar_arrive(&sm.full[g][0]);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        tc::fence_proxy_async_smem();
+        named_bar(1 + g, PT_GROUP);
+        if (lg == 0) tc::mbar_arrive(&sm.full[g][1]);
       }
     }
     cp_async_wait_all();
     // drain: no TMA write of this CTA may be in flight when the CTA exits
-    if (lg == 0 && issued > 0) tc::mbar_wait(&sm.full[g], (issued - 1) & 1);
-  } else if (warp == PT_QW) {
-    // ------------------------------------------------------------------ queries of each segment
+    if (lg == 0 && n_lo > 0) tc::mbar_wait(&sm.full[g][0], (n_lo - 1) & 1);
+    if (lg == 0 && n_hi > 0) tc::mbar_wait(&sm.full[g][1], (n_hi - 1) & 1);
+  } else if (warp == PT_SW) {
+    // ------------------------------------------------------------------ queries and S = Q K^T
+    // The whole warp runs the loop (descriptors stay warp-uniform), one elected lane issues.  S
+    // and PV have a warp each: every wait is then the one thing its warp waits for.  (One warp
+    // that polled all barriers lost 800 to 2500 cycles per batch: under the MMAs' operand
+    // traffic each test of a barrier takes hundreds.)
+    constexpr uint32_t ID_S = tc::idesc(tc::FMT_BF16, tc::FMT_BF16, PT_HC, PT_ROWS);
+    const uint64_t q_d = tc::desc_k_sw128(tc::smem_u32(sm.q[0]));
+    const uint64_t k_d0 = tc::desc_k_sw128(tc::smem_u32(sm.kv[0][0])), k_d1 = tc::desc_k_sw128(tc::smem_u32(sm.kv[1][0]));
     if (lane == 0) {
       tc::prefetch_tmap(&maps.q);
       tc::prefetch_tmap(&maps.pages);
       tc::prefetch_tmap(&maps.win);
-      int n = 0;
-      for (; seg.next(a); ++n) {
-        // the segment before no longer reads Q: its last S is complete
-        if (n > 0 && !(tc::mbar_wait(&sm.qfree, (n - 1) & 1) && !*(volatile int*)&sm.abort_flag)) break;
+    }
+    bool ok = true;
+    int n = 0, i = 0;
+    for (; ok && seg.next(a); ++n) {
+      // the segment before no longer reads Q once its last S is complete
+      if (n > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.qfree, (n - 1) & 1))) { ok = false; break; }
+      if (tc::elect_one()) {
         tc::mbar_arrive_expect_tx(&sm.qfull, PT_ATOMS * PT_HC * 128);
         for (int at = 0; at < PT_ATOMS; ++at)
           tc::tma_load_2d(sm.q[at], &maps.q, &sm.qfull, 64 * at, seg.b * a.H + hh * PT_HC);
       }
-      if (n > 0) tc::mbar_wait(&sm.qfull, (n - 1) & 1);
+      __syncwarp();
+      for (int64_t t = seg.t0; t < seg.t1; ++i) {
+        // The first turn issues nothing (live = 0): while the first tile loads, it brings the
+        // instructions in; cold, the first S took 4 us, later ones 1.
+        const uint32_t live = i > 0;
+        const int x = i - 1, st = x & 1;
+        const uint32_t ph = (x >> 1) & 1, d = tmem + TM_S + st * 32;
+        const uint64_t kd = st ? k_d1 : k_d0;
+        // (the tile's S buffer is free: its stage was refilled after the PV that used it)
+        bool go = !live || ((t > seg.t0 || tc::mbar_wait(&sm.qfull, n & 1)) && tc::mbar_wait(&sm.full[st][0], ph));
+        ok = __all_sync(0xffffffffu, go && !*(volatile int*)&sm.abort_flag);
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int at = 0; at < PT_LO; ++at)            // 4 steps of 16 dims an atom; atoms are 8 KB apart
+          tc::mma_f16_ws_x4<2>(d, q_d + (uint64_t)(at * (ATOM >> 4)), kd + (uint64_t)(at * (ATOM >> 4)), ID_S, at > 0, live);
+        ok = __all_sync(0xffffffffu, !live || tc::mbar_wait(&sm.full[st][1], ph));
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int at = PT_LO; at < PT_ATOMS; ++at)
+          tc::mma_f16_ws_x4<2>(d, q_d + (uint64_t)(at * (ATOM >> 4)), kd + (uint64_t)(at * (ATOM >> 4)), ID_S, 1, live);
+        if (live) {
+          ++t;
+          if (tc::elect_one()) {
+            tc::mma_commit(&sm.sfull[st]);
+            if (t == seg.t1) tc::mma_commit(&sm.qfree);
+          }
+        }
+        __syncwarp();
+      }
     }
+    if (!ok && lane == 0) atomicExch(&sm.abort_flag, 1);
+    // no copy of the queries and no MMA is in flight when the CTA frees TMEM and exits
+    if (n > 0 || !ok) tc::mbar_wait(&sm.qfull, (ok ? n - 1 : n) & 1);
+    if (tc::elect_one()) tc::mma_commit(&sm.drain[0]);
     __syncwarp();
-  } else if (warp == PT_MMAW) {
-    // ------------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop (descriptors stay warp-uniform); lane 0 decides, one
-    // elected lane (always the same) issues every MMA and commit.
-    constexpr uint32_t ID_S = tc::idesc(tc::FMT_BF16, tc::FMT_BF16, PT_HC, PT_ROWS);
+    tc::mbar_wait(&sm.drain[0], 0);
+  } else if (warp == PT_PVW) {
+    // ------------------------------------------------------------------ O (+)= (P_hi + P_lo) V
+    // Value dims 0-255 (atoms 0-3), then 256-511 (atoms 4-7), so that the first half of the stage
+    // is free early.  The two parts of P are two K ranges over the same V rows (a K step is 16
+    // rows of 128 bytes).
     constexpr uint32_t ID_O = tc::idesc(tc::FMT_BF16, tc::FMT_BF16, PT_HC, 256, 0, 1);
-    const uint64_t q_d0 = tc::desc_k_sw128(tc::smem_u32(sm.q[0]));
-    const uint64_t k_d0 = tc::desc_k_sw128(tc::smem_u32(sm.kv[0][0])), k_d1 = tc::desc_k_sw128(tc::smem_u32(sm.kv[1][0]));
-    const uint64_t p_d0 = tc::desc_k_sw128(tc::smem_u32(sm.p));
+    const uint64_t p_d = tc::desc_k_sw128(tc::smem_u32(sm.p));
     const uint64_t pl_d0 = tc::desc_k_sw128(tc::smem_u32(sm.kv[0][PT_ATOMS - 1])),
                    pl_d1 = tc::desc_k_sw128(tc::smem_u32(sm.kv[1][PT_ATOMS - 1]));
     const uint64_t v_d0 = tc::desc_mn_sw128(tc::smem_u32(sm.kv[0][0]), ATOM, 1024),
                    v_d1 = tc::desc_mn_sw128(tc::smem_u32(sm.kv[1][0]), ATOM, 1024);
-    // Event-driven: S(ns) once its tile has landed and its buffer is free (and, at a
-    // segment's first tile, its queries); PV(np) once P(np) is ready (and, at a first tile,
-    // the epilogue before has read O).  s_* and p_*: the walks of the two over the segments.
-    int ns = 0, np = 0;
-    SegIter ps = seg;
-    int s_seg = 0, p_seg = 0;
-    int64_t s_left = 0, p_left = 0;
-    bool s_first = true, p_first = true;
-    bool s_more = seg.next(a), p_more = ps.next(a);
-    if (s_more) { s_left = seg.t1 - seg.t0; p_left = s_left; }
-    uint64_t t_idle = tc::now_ns();
-    uint32_t spins = 0;
     bool ok = true;
-    while (ok && p_more) {
-      bool prog = false;
-      if (s_more) {
-        const int st = ns & 1;
-        const uint32_t ph = (ns >> 1) & 1;
-        bool ready = false;
-        if (lane == 0)
-          ready = tc::mbar_try_wait(&sm.full[st], ph) && tc::mbar_try_wait(&sm.sfree[st], ph ^ 1) &&
-                  (!s_first || tc::mbar_try_wait(&sm.qfull, s_seg & 1));
-        if (__shfl_sync(0xffffffffu, (int)ready, 0)) {
-          tc::fence_after_sync();
-          const uint32_t d = tmem + TM_S + st * 32;
-          const uint64_t kd = st ? k_d1 : k_d0;
-          if (tc::elect_one()) tc::mma_f16_ws<false>(d, q_d0, kd, ID_S);
-#pragma unroll
-          for (int i = 1; i < PT_ATOMS * 4; ++i) {
-            const uint64_t off = (uint64_t)(((i >> 2) * ATOM + (i & 3) * 32) >> 4);
-            if (tc::elect_one()) tc::mma_f16_ws<true>(d, q_d0 + off, kd + off, ID_S);
-          }
-          s_first = false;
-          const bool last = --s_left == 0;
+    int n = 0, i = 0;
+    for (; ok && seg.next(a); ++n) {
+      for (int64_t t = seg.t0; t < seg.t1; ++i) {
+        const uint32_t live = i > 0;                  // the first turn issues nothing, as above
+        const int x = i - 1, st = x & 1;
+        const uint64_t vd = st ? v_d1 : v_d0, pl = st ? pl_d1 : pl_d0;
+        const bool first = t == seg.t0;               // overwrites O, which the epilogue before has read
+        const bool go = !live || ((!first || n == 0 || tc::mbar_wait(&sm.ofree, (n - 1) & 1)) && tc::mbar_wait(&sm.pfull, x & 1));
+        ok = __all_sync(0xffffffffu, go && !*(volatile int*)&sm.abort_flag);
+        if (!ok) break;
+        tc::fence_after_sync();
+        tc::mma_f16_ws_x4<128>(tmem + TM_O, p_d, vd, ID_O, !first, live);
+        tc::mma_f16_ws_x4<128>(tmem + TM_O, pl, vd, ID_O, 1, live);
+        if (live && tc::elect_one()) tc::mma_commit(&sm.empty[st][0]);
+        __syncwarp();
+        const uint64_t vh = vd + (uint64_t)(PT_LO * (ATOM >> 4));
+        tc::mma_f16_ws_x4<128>(tmem + TM_O + 128, p_d, vh, ID_O, !first, live);
+        tc::mma_f16_ws_x4<128>(tmem + TM_O + 128, pl, vh, ID_O, 1, live);
+        if (live) {
+          ++t;
           if (tc::elect_one()) {
-            tc::mma_commit(&sm.sfull[st]);
-            if (last) tc::mma_commit(&sm.qfree);
-          }
-          __syncwarp();
-          ++ns;
-          if (last) {
-            s_more = seg.next(a);
-            s_left = seg.t1 - seg.t0;
-            s_first = true;
-            ++s_seg;
-          }
-          prog = true;
-        }
-      }
-      if (np < ns) {
-        bool ready = false;
-        if (lane == 0)
-          ready = tc::mbar_try_wait(&sm.pfull, np & 1) && (!p_first || p_seg == 0 || tc::mbar_try_wait(&sm.ofree, (p_seg - 1) & 1));
-        if (__shfl_sync(0xffffffffu, (int)ready, 0)) {
-          const int st = np & 1;
-          tc::fence_after_sync();
-          const uint64_t vd = st ? v_d1 : v_d0;
-          const uint64_t pl = st ? pl_d1 : pl_d0;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint64_t vh = vd + (uint64_t)((4 * half * ATOM) >> 4);
-            const uint32_t d = tmem + TM_O + 128 * half;
-            if (tc::elect_one()) {
-              if (p_first) tc::mma_f16_ws<false>(d, p_d0, vh, ID_O);
-              else tc::mma_f16_ws<true>(d, p_d0, vh, ID_O);
-            }
-#pragma unroll
-            for (int ks = 1; ks < PT_ROWS / 16; ++ks)
-              if (tc::elect_one()) tc::mma_f16_ws<true>(d, p_d0 + (uint64_t)((ks * 32) >> 4), vh + (uint64_t)((ks * 16 * 128) >> 4), ID_O);
-#pragma unroll
-            for (int ks = 0; ks < PT_ROWS / 16; ++ks)
-              if (tc::elect_one()) tc::mma_f16_ws<true>(d, pl + (uint64_t)((ks * 32) >> 4), vh + (uint64_t)((ks * 16 * 128) >> 4), ID_O);
-          }
-          if (tc::elect_one()) {
-            tc::mma_commit(&sm.empty[st]);
+            tc::mma_commit(&sm.empty[st][1]);
             tc::mma_commit(&sm.pdone);
           }
-          __syncwarp();
-          p_first = false;
-          ++np;
-          if (--p_left == 0) {
-            p_more = ps.next(a);
-            p_left = ps.t1 - ps.t0;
-            p_first = true;
-            ++p_seg;
-          }
-          prog = true;
         }
-      }
-      if (prog) {
-        spins = 0;
-      } else if ((++spins & 63u) == 0u) {
-        bool stop = false;
-        if (lane == 0) {
-          const uint64_t now = tc::now_ns();
-          if (spins == 64u) t_idle = now;
-          stop = *(volatile int*)&sm.abort_flag || now - t_idle > tc::WAIT_LIMIT_NS;
-        }
-        if (__shfl_sync(0xffffffffu, (int)stop, 0)) ok = false;
+        __syncwarp();
       }
     }
     if (!ok && lane == 0) atomicExch(&sm.abort_flag, 1);
-    // every MMA the elected lane issued has completed before the CTA frees TMEM
-    if (tc::elect_one()) tc::mma_commit(&sm.drain);
+    if (tc::elect_one()) tc::mma_commit(&sm.drain[1]);
     __syncwarp();
-    tc::mbar_wait(&sm.drain, 0);
+    tc::mbar_wait(&sm.drain[1], 0);
   } else {
     // ------------------------------------------------------------------ softmax + epilogue, warps 0-7
-    // Thread (wg, lane tl): head tl % 64; of S the tile rows 32 * (tl / 64) .. + 31, of which
-    // it exponentiates 16 (warpgroup wg's half); of O the dims 256 wg + 128 (tl / 64) .. + 127.
+    // Thread (wg, lane tl): head tl % 64; of S the tile rows 32 (tl / 64) + 16 wg .. + 15; of O
+    // the dims 256 wg + 128 (tl / 64) .. + 127.
     const int wg = warp >> 2, quarter = warp & 3;
     const int tl = quarter * 32 + lane;
     const int hl = tl & 63, half = tl >> 6;
     const int h = hh * PT_HC + hl;
     const bool hv = h < a.H;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    uint64_t* pairb = &sm.pairb[wg * 2 + (quarter & 1)];
+    uint64_t* const headb = &sm.headb[quarter & 1];
     // all softmax warps meet (a bounded wait, unlike a named barrier)
     uint32_t met = 0;
     auto meet = [&]() {
@@ -400,7 +408,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       return __all_sync(0xffffffffu, tc::mbar_wait(&sm.segb, met++ & 1));
     };
     // logits in the base-2 domain: P = 2^(s - m)
-    const float scale2 = a.sm_scale * 1.4426950408889634f;
+    const float scale2 = a.sm_scale * 1.4426950408889634f, scale = fabsf(scale2);
     bool ok = true;
     int i = 0;                                        // tiles so far, over all segments
     // sequences without a row (no unit has a tile of theirs)
@@ -411,72 +419,82 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (a.lse && tl < 64 && wg == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
     }
     __syncwarp();
+    if (threadIdx.x == 0 && hh == 0) paged_note(a, plan, unit);
     while (ok && seg.next(a)) {
       const float sink = hv ? a.sink[h] : 0.f;
       float m_run = -INFINITY, l_run = 0.f;           // running maximum; this thread's row sum
       for (int64_t t = seg.t0; t < seg.t1; ++t, ++i) {
         const int st = i & 1;
         const uint32_t ph = (i >> 1) & 1;
-        bool w = tc::mbar_wait(&sm.sfull[st], ph) && tc::mbar_wait(&sm.full[st], ph);
+        bool w = tc::mbar_wait(&sm.full[st][0], ph);  // the mask of the tile's rows
+        const uint32_t vm = sm.vmask[st][ph][half] >> (16 * wg);
+        w = w && tc::mbar_wait(&sm.sfull[st], ph);
         w = __all_sync(0xffffffffu, w && !*(volatile int*)&sm.abort_flag);
         if (!w) { ok = false; break; }
         tc::fence_after_sync();
-        float s[32];
+        float s[16];
         {
-          uint32_t v[32];
-          tc::tmem_ld16(tmem + lane_base + TM_S + st * 32, v);
-          tc::tmem_ld16(tmem + lane_base + TM_S + st * 32 + 16, v + 16);
+          uint32_t v[16];
+          tc::tmem_ld16(tmem + lane_base + TM_S + st * 32 + 16 * wg, v);
           tc::tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]) * scale2;
+          for (int j = 0; j < 16; ++j) s[j] = __uint_as_float(v[j]);
         }
         tc::fence_before_sync();
-        if (lane == 0) tc::mbar_arrive(&sm.sfree[st]);
-        const uint32_t vm = sm.vmask[st][half];
-        if (vm != 0xffffffffu) {
+        if (scale2 < 0.f) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < 16; ++j) s[j] = -s[j];
+        }
+        if ((vm & 0xffffu) != 0xffffu) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
             if (!((vm >> j) & 1u)) s[j] = -INFINITY;
         }
         float mq[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 4; j < 32; ++j) mq[j & 3] = fmaxf(mq[j & 3], s[j]);
-        float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        // the other half of the head's rows
-        sm.smax[st][wg][tl] = mt;
+        for (int j = 4; j < 16; ++j) mq[j & 3] = fmaxf(mq[j & 3], s[j]);
+        float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * scale;
+        // The tile's maximum over the head's four threads.  P is formed with the maximum so
+        // far while theirs arrive, and once more where it has to rise (lazily, by 2^8 at least).
+        float* const mx = sm.smax[st][0];
+        mx[wg * 128 + tl] = mt;
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(pairb);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(pairb, i & 1))) { ok = false; break; }
-        mt = fmaxf(mt, sm.smax[st][wg][tl ^ 64]);
-        // the running maximum is raised lazily, by all four threads of a head alike
+        if (lane == 0) tc::mbar_arrive(headb);
+        const bool p_free = i == 0 || tc::mbar_test(&sm.pdone, (i - 1) & 1);
         bool rescale = false;
-        float alpha = 1.f;
-        if (mt > m_run + PT_RESCALE || (m_run == -INFINITY && mt != -INFINITY)) {
-          const float m_new = fmaxf(mt, m_run);
-          alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
-          rescale = m_run != -INFINITY;
-          m_run = m_new;
-        }
-        const bool rescale_any = __any_sync(0xffffffffu, rescale);
+        float alpha = 1.f, psum;
         uint32_t w8[8], l8[8];
-        float psum = 0.f;
+        for (bool met_all = false;;) {
+          const float m0 = m_run == -INFINITY ? 0.f : m_run;
+          psum = 0.f;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float s0 = wg ? s[16 + 2 * u] : s[2 * u], s1 = wg ? s[17 + 2 * u] : s[2 * u + 1];
-          const float p0 = m_run == -INFINITY ? 0.f : ex2_approx(s0 - m_run);
-          const float p1 = m_run == -INFINITY ? 0.f : ex2_approx(s1 - m_run);
-          const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
-          const float h0 = __low2float(hb), h1 = __high2float(hb);
-          const __nv_bfloat162 lb = __floats2bfloat162_rn(p0 - h0, p1 - h1);
-          psum += (h0 + __low2float(lb)) + (h1 + __high2float(lb));    // the normaliser sums what the MMA sees
-          w8[u] = *reinterpret_cast<const uint32_t*>(&hb);
-          l8[u] = *reinterpret_cast<const uint32_t*>(&lb);
+          for (int u = 0; u < 8; ++u) {
+            const float p0 = ex2_approx(fmaf(s[2 * u], scale, -m0)), p1 = ex2_approx(fmaf(s[2 * u + 1], scale, -m0));
+            const __nv_bfloat162 hb = __floats2bfloat162_rn(p0, p1);
+            const __nv_bfloat162 lb = __floats2bfloat162_rn(p0 - __low2float(hb), p1 - __high2float(hb));
+            psum += p0 + p1;
+            w8[u] = *reinterpret_cast<const uint32_t*>(&hb);
+            l8[u] = *reinterpret_cast<const uint32_t*>(&lb);
+          }
+          if (met_all) break;
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(headb, i & 1))) { ok = false; break; }
+          met_all = true;
+          mt = fmaxf(fmaxf(mx[hl], mx[hl + 64]), fmaxf(mx[hl + 128], mx[hl + 192]));
+          const bool raise = mt > m_run + PT_RESCALE || (m_run == -INFINITY && mt != -INFINITY);
+          if (!__any_sync(0xffffffffu, raise)) break;
+          if (raise) {
+            const float m_new = fmaxf(mt, m_run);
+            alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
+            rescale = m_run != -INFINITY;
+            m_run = m_new;
+          }
         }
+        if (!ok) break;
+        const bool rescale_any = __any_sync(0xffffffffu, rescale);
         l_run = l_run * alpha + psum;
-        if (i > 0) {                                  // the PV before owns P and O until it completes
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.pdone, (i - 1) & 1))) { ok = false; break; }
-          tc::fence_after_sync();
-        }
+        // the PV before owns P and O until it completes
+        if (!__all_sync(0xffffffffu, p_free || tc::mbar_wait(&sm.pdone, (i - 1) & 1))) { ok = false; break; }
+        tc::fence_after_sync();
         if (rescale_any) {
 #pragma unroll 1
           for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
@@ -569,7 +587,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   tc::fence_before_sync();
   __syncthreads();
   if (sm.abort_flag && threadIdx.x == 0) raise_err(a.err, CSA_DEVERR_TIMEOUT);
-  if (warp == PT_MMAW) {
+  if (warp == PT_SW) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, TM_COLS);
   }
@@ -609,9 +627,9 @@ int paged_units_tc(int B, int H, int64_t rows_max) {
 
 cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
   const int halves = a.H > PT_HC ? 2 : 1;
-  a.units = paged_units_tc(a.B, a.H, paged_rows_max(a));
   a.tile = PT_ROWS;
   a.min_tiles = PT_MIN_TILES;
+  a.units = paged_units(a, paged_units_tc(a.B, a.H, paged_rows_max(a)));
   // the largest of 64, 32, 16, 8 rows that divides the pages: every box lies in one page
   int box = PT_ROWS;
   while (box >= 8 && a.page % box != 0) box >>= 1;

@@ -62,7 +62,7 @@ struct PagedPlan {
   int64_t total;     // tiles of all sequences
   int64_t per;       // tiles of a unit
   int64_t before;    // tiles of the sequences before sequence b
-  int b;             // the sequence that holds tile `at` (B when there is none)
+  int b;             // the sequence that holds the unit's first tile (B when there is none)
 };
 
 // The plan, and the sequence that holds tile unit * per.  All `threads` threads of the block
@@ -116,6 +116,30 @@ __host__ __device__ inline size_t paged_part_block(int H, int dv) { return (size
 __host__ __device__ inline size_t paged_part_val(int H, int h, int c) { return ((size_t)(c >> 2) * H + h) * 4 + (c & 3); }
 __host__ __device__ inline size_t paged_part_rec(int H, int dv, int h) { return (size_t)dv * H + 4 * (size_t)h; }
 
+// After the partials, one note per unit: {b, n} when sequence b begins in the unit and goes on
+// in the n - 1 units after it, {-, 0} otherwise.
+__host__ __device__ inline int2* paged_notes(const PagedAttnArgs& a) {
+  return reinterpret_cast<int2*>(a.part + 2 * (size_t)a.units * paged_part_block(a.H, a.dv));
+}
+// Writes the unit's note (one thread).
+__device__ __forceinline__ void paged_note(const PagedAttnArgs& a, const PagedPlan& p, int unit) {
+  const int64_t end = (int64_t)(unit + 1) * p.per;    // first tile of the next unit
+  int2 note = make_int2(-1, 0);
+  if (end < p.total) {
+    int64_t at = p.before;
+    int b = p.b;
+    for (;; ++b) {                                    // the sequence that holds tile end - 1
+      const int64_t n = paged_tiles(a, b);
+      if (end - 1 < at + n) {
+        if (end < at + n && at >= end - p.per) note = make_int2(b, (int)((at + n - 1) / p.per) - unit + 1);
+        break;
+      }
+      at += n;
+    }
+  }
+  paged_notes(a)[unit] = note;
+}
+
 // Row v of segment A (entries or index slots) of sequence b: its row in the pool, or -1
 // (an unused slot, or a bad entry or page, which sets CSA_DEVERR_INDEX).
 __device__ __forceinline__ int64_t paged_row(const PagedAttnArgs& a, int b, int v) {
@@ -138,7 +162,16 @@ inline int paged_units(int ctas, int B, int64_t rows_max, int tile, int min_tile
   const int64_t u = (tiles + min_tiles - 1) / min_tiles;
   return (int)(u < ctas ? (u < 1 ? 1 : u) : (ctas < 1 ? 1 : ctas));
 }
-inline size_t paged_slots(int units) { return 2 * (size_t)units; }
+// The launch knows entries and window apart: at most this many units of the above are of use.
+inline int paged_units(const PagedAttnArgs& a, int units) {
+  const int64_t rows = a.idx ? (int64_t)a.k : paged_capacity(a);
+  const int64_t tiles = a.B * ((rows + a.tile - 1) / a.tile + (a.W + a.tile - 1) / a.tile);
+  const int64_t u = (tiles + a.min_tiles - 1) / a.min_tiles;
+  return (int)(u < units ? (u < 1 ? 1 : u) : units);
+}
+inline size_t paged_ws_bytes(int units, int H, int dv) {
+  return 2 * (size_t)units * paged_part_block(H, dv) * sizeof(float) + (size_t)units * sizeof(int2);
+}
 // Rows that one sequence may have: the workspace size and the launch use the same number.
 inline int64_t paged_rows_max(const PagedAttnArgs& a) { return (a.idx ? (int64_t)a.k : paged_capacity(a)) + a.W; }
 int paged_units_cc(int B, int H, int64_t rows_max);
