@@ -12,6 +12,8 @@
 // This path takes every shape and both storage types in fp32 arithmetic.
 #include "paged.cuh"
 
+#include <cuda_fp16.h>
+
 namespace csa {
 
 namespace {
@@ -158,9 +160,9 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
         if (c < dv) *reinterpret_cast<float4*>(blk + paged_part_val(a.H, h, c)) = o[i];
       }
       if (lane == 0) {
-        float* rec = blk + paged_part_rec(a.H, dv, h);
-        rec[0] = m_run;
-        rec[1] = l_run;
+        float4* rec = reinterpret_cast<float4*>(blk + paged_part_rec(a.H, dv, h));
+        rec[0] = make_float4(m_run, l_run, 1.f, 1.f);
+        rec[1] = make_float4(1.f, 1.f, 0.f, 0.f);
       }
     }
   }
@@ -169,16 +171,19 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
 // Joins the pieces of cut sequences: out = sum_p e^{m_p - M} o_p / (e^{sink - M} +
 // sum_p e^{m_p - M} l_p).  The units noted which sequences they began and did not finish;
 // every CTA gathers those notes and takes its share of the items (sequence, eight heads,
-// slice of the dims), the slices as narrow as it takes to give every CTA an item.  Thread
-// (head, 16-byte piece of dims): eight heads' pieces of a partial are one 128-byte line.
-// The pieces are added in order, so a result does not depend on the order in which the
-// units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece.
-constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 8;
-template <typename T>
-__global__ void __launch_bounds__(PM_THREADS)
+// slice of the dims), the slices as narrow as it takes to give every CTA an item.  Eight
+// heads' 16-byte pieces of a partial are one 128-byte line.  Where a slice leaves threads
+// over, they share its pieces.  All sums run in a fixed order, so a result does not depend
+// on the order in which the units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece, and
+// the latency of its few round trips.
+constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 8, PM_PER_SM = 3;
+template <typename T, bool PART16>
+__global__ void __launch_bounds__(PM_THREADS, PM_PER_SM)
 paged_merge_kernel(PagedAttnArgs a) {
-  extern __shared__ float wts[];                     // [units][8] e^{m_p - M} / den, then the list
-  __shared__ float red[PM_THREADS / 32][PM_H];
+  constexpr int V = PART16 ? 8 : 4;                  // dims of a 16-byte piece
+  extern __shared__ float4 wts[];                    // [piece][8] e^{m_p - M} times the quarters' powers, then the list
+  __shared__ float red[2][PM_THREADS / 32][PM_H];
+  __shared__ float sums[V][PM_THREADS];
   __shared__ int count;
   int* list = reinterpret_cast<int*>(wts + (size_t)a.units * PM_H);
   const int dv = a.dv, H = a.H;
@@ -197,81 +202,132 @@ paged_merge_kernel(PagedAttnArgs a) {
     if (lane == 0) count = n;
   }
   __syncthreads();
-  const int hb = (H + PM_H - 1) / PM_H, c4 = dv / 4;
+  const int hb = (H + PM_H - 1) / PM_H, pieces = dv / V;
   int slices = 1;
-  while (slices < PM_SLICES && count * hb * slices < (int)gridDim.x) slices <<= 1;
-  const int width = (c4 + slices - 1) / slices;       // 16-byte pieces of a slice
+  while (slices < PM_SLICES && 2 * count * hb * slices <= (int)gridDim.x && pieces / slices > 4) slices <<= 1;
+  const int width = (pieces + slices - 1) / slices;   // 16-byte pieces of a slice
+  int gw = PM_C;                                      // threads along a slice; the other PM_C / gw share its partials
+  while (gw > 4 && gw / 2 >= width) gw >>= 1;
+  const int groups = PM_C / gw, g = j / gw, jc = j - g * gw;
   for (int item = blockIdx.x; item < count * hb * slices; item += gridDim.x) {
     const int sl = item % slices, blk8 = item / slices % hb, unit = list[item / (slices * hb)];
     const int2 note = __ldcg(&notes[unit]);
     const int b = note.x, n = note.y, h = blk8 * PM_H + hl;
     const bool hv = h < H;
-    // piece 0 lies in slot 1 of the unit, piece p > 0 in slot 0 of unit + p
+    const int hc = hv ? h : H - 1;
+    // partial 0 lies in slot 1 of the unit, partial p > 0 in slot 0 of unit + p
     const size_t block = paged_part_block(H, dv);
-    const float* first = a.part + (size_t)(2 * unit + 1) * block;
-    const float* rest = a.part + (size_t)(2 * unit) * block;                // + 2 p blocks
-    auto across = [&](float v, bool mx) {             // over the threads of a head
-#pragma unroll
-      for (int o = PM_H; o < 32; o <<= 1) {
-        const float w = __shfl_xor_sync(0xffffffffu, v, o);
-        v = mx ? fmaxf(v, w) : v + w;
-      }
-      __syncthreads();
-      if (lane < PM_H) red[warp][lane] = v;
-      __syncthreads();
-      float r = red[0][hl];
-#pragma unroll
-      for (int w = 1; w < PM_THREADS / 32; ++w) r = mx ? fmaxf(r, red[w][hl]) : r + red[w][hl];
-      return r;
+    const float* part = a.part + (size_t)(2 * unit) * block;
+    auto partial = [&](int p) { return part + (p ? 2 * p * block : block); };
+    auto load = [&](int p, int c) {
+      return __ldcg(reinterpret_cast<const uint4*>(partial(p)) + (size_t)c * H + hc);
     };
-    const float sk = hv ? a.sink[h] : -INFINITY;
+    const int c0 = sl * width + jc, c1 = min(pieces, (sl + 1) * width);
+    // the group's first partials are on their way while the weights are formed
+    uint4 x[PM_EARLY];
+#pragma unroll
+    for (int u = 0; u < PM_EARLY; ++u)
+      if (g + u * groups < n && c0 < c1) x[u] = load(g + u * groups, c0);
+    const float sk = a.sink[hc];
+    const size_t rec = paged_part_rec(H, dv, hc);
     float M = sk;
-    const size_t rec = paged_part_rec(H, dv, hv ? h : 0);
-    for (int p = j; p < n; p += PM_C) M = fmaxf(M, __ldcg((p ? rest + 2 * p * block : first) + rec));
-    M = across(M, true);
+    for (int p = j; p < n; p += PM_C) {
+      const float4 r = __ldcg(reinterpret_cast<const float4*>(partial(p) + rec));
+      wts[p * PM_H + hl] = r;
+      M = fmaxf(M, r.x);
+    }
+#pragma unroll
+    for (int o = PM_H; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane < PM_H) red[0][warp][lane] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < PM_THREADS / 32; ++w) M = fmaxf(M, red[0][w][hl]);
     float den = 0.f;
     for (int p = j; p < n; p += PM_C) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>((p ? rest + 2 * p * block : first) + rec));
-      const float w = ml.x == -INFINITY ? 0.f : __expf(ml.x - M);
-      den += w * ml.y;
-      wts[p * PM_H + hl] = w;
-    }
-    den = across(den, false) + (sk == -INFINITY ? 0.f : __expf(sk - M));
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    for (int c = sl * width + j; c < min(c4, (sl + 1) * width) && hv; c += PM_C) {
-      const size_t at = paged_part_val(H, h, 4 * c);
-      float4 x = __ldcg(reinterpret_cast<const float4*>(first + at));
-      float w = wts[hl];
-      float4 acc = make_float4(w * x.x, w * x.y, w * x.z, w * x.w);
-#pragma unroll 8
-      for (int p = 1; p < n; ++p) {
-        x = __ldcg(reinterpret_cast<const float4*>(rest + 2 * p * block + at));
-        w = wts[p * PM_H + hl];
-        acc.x = fmaf(w, x.x, acc.x);
-        acc.y = fmaf(w, x.y, acc.y);
-        acc.z = fmaf(w, x.z, acc.z);
-        acc.w = fmaf(w, x.w, acc.w);
+      const float4 r = wts[p * PM_H + hl];            // {m, l, s0, s1}, this thread's own
+      const float w = r.x == -INFINITY ? 0.f : __expf(r.x - M);
+      den += w * r.y;
+      float4 q = make_float4(w, w, w, w);
+      if (PART16) {
+        const float2 s = __ldcg(reinterpret_cast<const float2*>(partial(p) + rec + 4));
+        q = make_float4(w * r.z, w * r.w, w * s.x, w * s.y);
       }
-      T* dst = (T*)a.out + ((size_t)b * H + h) * dv + 4 * c;
-      Elem<T>::st(dst, acc.x * inv);
-      Elem<T>::st(dst + 1, acc.y * inv);
-      Elem<T>::st(dst + 2, acc.z * inv);
-      Elem<T>::st(dst + 3, acc.w * inv);
+      wts[p * PM_H + hl] = q;
+    }
+#pragma unroll
+    for (int o = PM_H; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane < PM_H) red[1][warp][lane] = den;
+    __syncthreads();
+    den = sk == -INFINITY ? 0.f : __expf(sk - M);
+#pragma unroll
+    for (int w = 0; w < PM_THREADS / 32; ++w) den += red[1][w][hl];
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    for (int c = c0; c - jc < c1; c += gw) {
+      float acc[V];
+#pragma unroll
+      for (int u = 0; u < V; ++u) acc[u] = 0.f;
+      const float* wq = reinterpret_cast<const float*>(wts) + 4 * hl + (PART16 ? (c >> 4) & 3 : 0);   // 16 pieces a quarter
+      auto add = [&](const uint4& v, int p) {
+        const float w = wq[p * PM_H * 4];
+        const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (PART16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u4[q]));
+            acc[2 * q % V] = fmaf(w, f.x, acc[2 * q % V]);
+            acc[(2 * q + 1) % V] = fmaf(w, f.y, acc[(2 * q + 1) % V]);
+          } else {
+            acc[q] = fmaf(w, __uint_as_float(u4[q]), acc[q]);
+          }
+        }
+      };
+      if (c < c1) {
+        if (c != c0) {
+#pragma unroll
+          for (int u = 0; u < PM_EARLY; ++u)
+            if (g + u * groups < n) x[u] = load(g + u * groups, c);
+        }
+#pragma unroll
+        for (int u = 0; u < PM_EARLY; ++u)
+          if (g + u * groups < n) add(x[u], g + u * groups);
+#pragma unroll 8
+        for (int p = g + PM_EARLY * groups; p < n; p += groups) add(load(p, c), p);
+      }
+      if (groups > 1) {                               // (the slice is one round of its threads)
+#pragma unroll
+        for (int u = 0; u < V; ++u) sums[u][threadIdx.x] = acc[u];
+        __syncthreads();
+        for (int o = 1; g == 0 && o < groups; ++o)
+#pragma unroll
+          for (int u = 0; u < V; ++u) acc[u] += sums[u][threadIdx.x + o * gw * PM_H];
+      }
+      if (g == 0 && c < c1 && hv) {
+        T* dst = (T*)a.out + ((size_t)b * H + h) * dv + V * c;
+#pragma unroll
+        for (int u = 0; u < V; ++u) acc[u] *= inv;
+        if constexpr (V == Elem<T>::VEC) {
+          Elem<T>::st_vec(dst, acc);
+        } else {
+#pragma unroll
+          for (int u = 0; u < V; ++u) Elem<T>::st(dst + u, acc[u]);
+        }
+      }
     }
     if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+    __syncthreads();                                  // the weights and sums are read
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, cudaStream_t st) {
   if (a.units == 1) return cudaSuccess;                // nothing is ever cut
   const int64_t most = (int64_t)(a.units - 1) * ((a.H + PM_H - 1) / PM_H) * PM_SLICES;
-  const int grid = 2 * num_sms();
+  const int grid = PM_PER_SM * num_sms();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(most < grid ? most : grid));
   cfg.blockDim = dim3(PM_THREADS);
-  cfg.dynamicSmemBytes = (size_t)a.units * (PM_H * sizeof(float) + sizeof(int));   // a sequence has at most `units` pieces
+  cfg.dynamicSmemBytes = (size_t)a.units * (PM_H * sizeof(float4) + sizeof(int));  // a sequence has at most `units` pieces
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the pieces first of all
@@ -279,8 +335,9 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   note_launch();
-  return dtype == CSA_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, a)
-                           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, a);
+  if (part16) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, true>, a);
+  return dtype == CSA_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, false>, a)
+                           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<float, false>, a);
 }
 
 // Two CTAs per SM over the head groups.
@@ -304,7 +361,7 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
     paged_attn_cc_kernel<T><<<grid, warps * 32, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_paged_merge(a, dtype, st);
+    return launch_paged_merge(a, dtype, false, st);
   };
   return dtype == CSA_BF16 ? go(__nv_bfloat16()) : go(float());
 }
