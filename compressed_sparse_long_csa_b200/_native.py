@@ -81,7 +81,8 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the address alone (torch.cuda.current_stream() builds a Stream object: 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -319,23 +320,32 @@ def sparse_attn_decode_noalloc(q, cache, idx, win, win_len, sink, sm_scale, d_v,
 
 
 # ---- paged cache.  The tensors' shapes, types, strides and device are checked here (the C
-# calls see addresses only): what does not fit raises CsaError and nothing is launched.
-def _want(name, what, t, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise CsaError(f"{name}: {what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                       f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+# calls see addresses only): what does not fit raises CsaError and nothing is launched.  A
+# decode step makes these calls once per layer, so the checks are kept to a few plain
+# comparisons a tensor; the message is made when one fails.
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
+def _unfit(name, what, want):
+    raise CsaError(f"{name}: {what} must be {want}")
+
+
+def _want(name, what, t, dtype, shape, di):
+    if t.dtype != dtype or t.shape != shape or t.get_device() != di or not t.is_contiguous():
+        _unfit(name, what, f"a contiguous {dtype} tensor of shape {tuple(shape)} on the pages' device, got {t.dtype} "
+                           f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _paged(name, pages, block_table):
-    """Checks of the pool and its table; the device of the call."""
-    dev = pages.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise CsaError(f"{name}: pages must be on the current CUDA device, got {dev}")
-    if pages.dim() != 3 or not pages.is_contiguous() or pages.dtype not in (torch.bfloat16, torch.float32):
-        raise CsaError(f"{name}: pages must be a contiguous bf16 or fp32 tensor [n_pages, page_size, d]")
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev or not block_table.is_contiguous():
-        raise CsaError(f"{name}: block_table must be a contiguous int32 tensor [B, table_width] on {dev}")
-    return dev
+    """Checks of the pool and its table; the device's index."""
+    di = pages.get_device()
+    if di < 0 or di != torch.cuda.current_device():
+        _unfit(name, "pages", f"on the current CUDA device, got {pages.device}")
+    if pages.dim() != 3 or not pages.is_contiguous() or (pages.dtype != _BF16 and pages.dtype != _F32):
+        _unfit(name, "pages", "a contiguous bf16 or fp32 tensor [n_pages, page_size, d]")
+    if block_table.dim() != 2 or block_table.dtype != _I32 or block_table.get_device() != di or not block_table.is_contiguous():
+        _unfit(name, "block_table", "a contiguous int32 tensor [B, table_width] on the pages' device")
+    return di
 
 
 def latent_append_paged(rows, entry, pages, block_table, seq=None, pos=None, inv_freq=None, interleaved=True, q_pe=None,
@@ -345,82 +355,97 @@ def latent_append_paged(rows, entry, pages, block_table, seq=None, pos=None, inv
     rotary parts q_pe [T, H, d_r] rotated into the last d_r values of q [T, H, d_q].  rows and q_pe may
     be strided in all but their last dimension.  See csa.h."""
     name = "latent_append_paged"
-    dev = _paged(name, pages, block_table)
+    di = _paged(name, pages, block_table)
     n_pages, page, d = pages.shape
     B, width = block_table.shape
-    T = entry.shape[0] if entry.dim() == 1 else -1
     dt = pages.dtype
-    _want(name, "entry", entry, torch.int32, (T,), dev)
-    if rows.shape != (T, d) or rows.dtype != dt or rows.device != dev or (d > 1 and rows.stride(1) != 1):
-        raise CsaError(f"{name}: rows must be [{T}, {d}] {dt} on {dev} with a dense last dimension")
+    if entry.dim() != 1:
+        _unfit(name, "entry", "an int32 tensor [T]")
+    T = entry.shape[0]
+    of_T = (T,)
+    _want(name, "entry", entry, _I32, of_T, di)
+    if rows.shape != (T, d) or rows.dtype != dt or rows.get_device() != di or (d > 1 and rows.stride(1) != 1):
+        _unfit(name, "rows", f"[{T}, {d}] {dt} on the pages' device with a dense last dimension")
+    ld = rows.stride(0) if T > 1 else d
+    sp = pp = fp = qp = qo = None
+    d_r = H = d_q = ld_t = ld_h = 0
     if seq is not None:
-        _want(name, "seq", seq, torch.int32, (T,), dev)
+        _want(name, "seq", seq, _I32, of_T, di)
+        sp = seq.data_ptr()
     if pos is not None:
-        _want(name, "pos", pos, torch.int32, (T,), dev)
-    d_r = 0
+        _want(name, "pos", pos, _I32, of_T, di)
+        pp = pos.data_ptr()
     if inv_freq is not None:
         d_r = 2 * inv_freq.numel()
-        _want(name, "inv_freq", inv_freq, torch.float32, (d_r // 2,), dev)
-    H = d_q = ld_t = ld_h = 0
+        _want(name, "inv_freq", inv_freq, _F32, (d_r // 2,), di)
+        fp = inv_freq.data_ptr()
     if (q is None) != (q_pe is None):
-        raise CsaError(f"{name}: q and q_pe come together")
+        _unfit(name, "q", "given together with q_pe")
     if q is not None:
-        H, d_q = (q.shape[1], q.shape[2]) if q.dim() == 3 else (-1, -1)
-        _want(name, "q", q, dt, (T, H, d_q), dev)
-        if q_pe.shape != (T, H, d_r) or q_pe.dtype != dt or q_pe.device != dev or q_pe.stride(2) != 1:
-            raise CsaError(f"{name}: q_pe must be [{T}, {H}, {d_r}] {dt} on {dev} with a dense last dimension")
-        ld_t, ld_h = q_pe.stride(0), q_pe.stride(1)
-    ld = rows.stride(0) if T > 1 else d
-    _check(lib.latent_append_paged(rows.data_ptr(), ld, _p(seq), entry.data_ptr(), _p(pos), _p(inv_freq), d_r,
-                                   int(interleaved), pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, B, T,
-                                   d, _p(q_pe), ld_t, ld_h, _p(q), H, d_q, _dtype_code(pages), _stream(stream)), name)
+        if q.dim() != 3:
+            _unfit(name, "q", "[T, H, d_q]")
+        _, H, d_q = q.shape
+        _want(name, "q", q, dt, (T, H, d_q), di)
+        if q_pe.shape != (T, H, d_r) or q_pe.dtype != dt or q_pe.get_device() != di or q_pe.stride(2) != 1:
+            _unfit(name, "q_pe", f"[{T}, {H}, {d_r}] {dt} on the pages' device with a dense last dimension")
+        ld_t, ld_h, _ = q_pe.stride()
+        qp, qo = q_pe.data_ptr(), q.data_ptr()
+    _check(lib.latent_append_paged(rows.data_ptr(), ld, sp, entry.data_ptr(), pp, fp, d_r, 1 if interleaved else 0,
+                                   pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, B, T, d, qp, ld_t, ld_h,
+                                   qo, H, d_q, CSA_BF16 if dt == _BF16 else CSA_F32, _stream(stream)), name)
 
 
 def attn_decode_paged_workspace_size(B, H, d_v, rows_max):
     return int(lib.attn_decode_paged_workspace_size(B, H, d_v, rows_max))
 
 
-def _paged_attn(name, q, pages, block_table, sel, sel_shape, win, win_len, sink, d_v, out, lse, workspace):
-    """Checks of a paged attention call; (B, H, d_k, W, workspace address, bytes)."""
-    dev = _paged(name, pages, block_table)
-    d_k = pages.shape[2]
-    B = block_table.shape[0]
-    H = q.shape[1] if q.dim() == 3 else -1
+def _paged_attn(name, call, q, pages, block_table, sel, sparse, win, win_len, sink, sm_scale, d_v, out, lse, workspace, stream):
+    di = _paged(name, pages, block_table)
+    n_pages, page, d_k = pages.shape
+    B, width = block_table.shape
     dt = pages.dtype
-    _want(name, "q", q, dt, (B, H, d_k), dev)
-    _want(name, "out", out, dt, (B, H, d_v), dev)
-    _want(name, "sink", sink, torch.float32, (H,), dev)
-    _want(name, "n_entries" if len(sel_shape) == 1 else "idx", sel, torch.int32, sel_shape, dev)
-    W = 0
+    if q.dim() != 3:
+        _unfit(name, "q", "[B, H, d_k]")
+    H = q.shape[1]
+    _want(name, "q", q, dt, (B, H, d_k), di)
+    _want(name, "out", out, dt, (B, H, d_v), di)
+    _want(name, "sink", sink, _F32, (H,), di)
+    if sparse:
+        if sel.dim() != 2:
+            _unfit(name, "idx", "[B, k]")
+        k = sel.shape[1]
+        _want(name, "idx", sel, _I32, (B, k), di)
+        picked = (sel.data_ptr(), k)
+    else:
+        _want(name, "n_entries", sel, _I32, (B,), di)
+        picked = (sel.data_ptr(),)
+    W, wp, lp, ep = 0, None, None, None
     if win is not None:
-        W = win.shape[1] if win.dim() == 3 else -1
-        _want(name, "win", win, dt, (B, W, d_k), dev)
-        _want(name, "win_len", win_len, torch.int32, (B,), dev)
+        if win.dim() != 3 or win_len is None:
+            _unfit(name, "win", "[B, W, d_k] with win_len")
+        W = win.shape[1]
+        _want(name, "win", win, dt, (B, W, d_k), di)
+        _want(name, "win_len", win_len, _I32, (B,), di)
+        wp, lp = win.data_ptr(), win_len.data_ptr()
     if lse is not None:
-        _want(name, "lse", lse, torch.float32, (B, H), dev)
-    if workspace is None or workspace.device != dev or not workspace.is_contiguous():
-        raise CsaError(f"{name}: workspace must be a contiguous tensor on {dev}")
-    return B, H, d_k, W, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _want(name, "lse", lse, _F32, (B, H), di)
+        ep = lse.data_ptr()
+    if workspace is None or workspace.get_device() != di or not workspace.is_contiguous():
+        _unfit(name, "workspace", "a contiguous tensor on the pages' device")
+    _check(call(q.data_ptr(), pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, *picked, wp, lp,
+                sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, CSA_BF16 if dt == _BF16 else CSA_F32, out.data_ptr(), ep,
+                workspace.data_ptr(), workspace.nbytes, _stream(stream)), name)
 
 
 def hca_attn_decode_paged(q, pages, block_table, n_entries, win, win_len, sink, sm_scale, d_v, out, lse=None,
                           workspace=None, stream=None):
     """hca_attn_decode over a paged cache: pages [n_pages, page_size, d_k], block_table [B, table_width]."""
-    B, H, d_k, W, wp, wb = _paged_attn("hca_attn_decode_paged", q, pages, block_table, n_entries, block_table.shape[:1],
-                                       win, win_len, sink, d_v, out, lse, workspace)
-    _check(lib.hca_attn_decode_paged(q.data_ptr(), pages.data_ptr(), pages.shape[0], pages.shape[1],
-                                     block_table.data_ptr(), block_table.shape[1], n_entries.data_ptr(), _p(win),
-                                     _p(win_len), sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, _dtype_code(q),
-                                     out.data_ptr(), _p(lse), wp, wb, _stream(stream)), "hca_attn_decode_paged")
+    _paged_attn("hca_attn_decode_paged", lib.hca_attn_decode_paged, q, pages, block_table, n_entries, False, win, win_len,
+                sink, sm_scale, d_v, out, lse, workspace, stream)
 
 
 def sparse_attn_decode_paged(q, pages, block_table, idx, win, win_len, sink, sm_scale, d_v, out, lse=None,
                              workspace=None, stream=None):
     """sparse_attn_decode over a paged cache: idx [B, k] entry ids (-1 = unused slot)."""
-    k = idx.shape[1] if idx.dim() == 2 else -1
-    B, H, d_k, W, wp, wb = _paged_attn("sparse_attn_decode_paged", q, pages, block_table, idx,
-                                       (block_table.shape[0], k), win, win_len, sink, d_v, out, lse, workspace)
-    _check(lib.sparse_attn_decode_paged(q.data_ptr(), pages.data_ptr(), pages.shape[0], pages.shape[1],
-                                        block_table.data_ptr(), block_table.shape[1], idx.data_ptr(), k, _p(win),
-                                        _p(win_len), sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, _dtype_code(q),
-                                        out.data_ptr(), _p(lse), wp, wb, _stream(stream)), "sparse_attn_decode_paged")
+    _paged_attn("sparse_attn_decode_paged", lib.sparse_attn_decode_paged, q, pages, block_table, idx, True, win, win_len,
+                sink, sm_scale, d_v, out, lse, workspace, stream)

@@ -355,7 +355,8 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
   dim3 grid(a.units, (a.H + PC_WARPS - 1) / PC_WARPS);
   auto go = [&](auto tag) {
     using T = decltype(tag);
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_cc_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    static std::atomic<uint64_t> ready;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(paged_attn_cc_kernel<T>), ready, 96 * 1024);
     if (e != cudaSuccess) return e;
     note_launch();
     paged_attn_cc_kernel<T><<<grid, warps * 32, smem, st>>>(a);

@@ -662,7 +662,8 @@ cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
     maps.win = maps.pages;                           // no tile is ever a window tile
   }
   auto kern = a.idx ? paged_attn_tc_kernel<true> : paged_attn_tc_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PtSmem));
+  static std::atomic<uint64_t> ready[2];               // bit per device: the kernel's shared-memory size is set
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), ready[a.idx ? 1 : 0], (int)sizeof(PtSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(halves * a.units);

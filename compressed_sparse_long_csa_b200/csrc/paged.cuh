@@ -5,7 +5,22 @@
 #pragma once
 #include "common.cuh"
 
+#include <atomic>
+
 namespace csa {
+
+// Raises a kernel's dynamic shared-memory limit, once per device (`done`: a bit per device,
+// one word per kernel): the call takes longer on the host than all checks of a launch.
+inline cudaError_t set_smem_once(const void* kernel, std::atomic<uint64_t>& done, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);             // the library takes devices 0 .. 63
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct PagedAttnArgs {
   const void* q;              // [B, H, dk]
