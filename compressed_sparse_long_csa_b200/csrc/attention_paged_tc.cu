@@ -50,7 +50,8 @@ struct PtSmem {
   uint8_t p[PT_HC * 128];                    // P_hi: 64 heads x 64 rows bf16; between segments the row sums
   float smax[2][2][128];                     // per tile parity and warpgroup: the lanes' tile maxima
   int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
-  uint32_t vmask[2][2][2];                   // per stage and use parity: bit j of word j / 32: row j is valid
+  uint32_t vmask[2][4][2];                   // per stage and use of it mod 4 (a group's warps may be a tile apart, the
+                                             // softmax another behind): bit j of word j / 32 set when row j is valid
   uint64_t full[2][2], empty[2][2];          // per stage and half of the dims (0-255, 256-575)
   uint64_t sfull[2];
   uint64_t pfull, pdone, qfull, qfree, ofree, drain[2];
@@ -197,16 +198,8 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         }
       }
     };
-    // Brings the next tile's rows into the L2 while its stage is still in use.  By plain
-    // prefetches: the copy engine takes about as long for a prefetch as for the copy.
-    auto prefetch = [&]() {
-      if (lg >= PT_ROWS || y < 0) return;
-      const uint8_t* r = reinterpret_cast<const uint8_t*>(in_a ? a.pages : a.win) + (size_t)y * (576 * 2);
-#pragma unroll
-      for (int k = 0; k < PT_ATOMS; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * k));
-    };
     step(g);
-    if (more) { resolve(); if (g > 0) prefetch(); }
+    if (more) resolve();
     int n_lo = 0, n_hi = 0;                           // halves this group started (for the drain)
     for (int i = 0; more; ++i) {
       // what needs no free stage comes first: the rows, which of them exist, how they are copied
@@ -214,13 +207,13 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (lg < PT_ROWS) {
         sm.rowy[g][lg] = y;                           // (the group's copies of the tile before are issued)
         const uint32_t vb = __ballot_sync(0xffffffffu, y >= 0);
-        if ((lg & 31) == 0) sm.vmask[g][i & 1][lg >> 5] = vb;
+        if ((lg & 31) == 0) sm.vmask[g][i & 3][lg >> 5] = vb;
       }
       const bool a_tile = in_a;
       named_bar(1 + g, PT_GROUP);
       const int stop = *(volatile int*)&sm.ld_stop[g];
       if (stop != 0 && stop <= i + 1) break;
-      const bool all = (sm.vmask[g][i & 1][0] & sm.vmask[g][i & 1][1]) == 0xffffffffu;
+      const bool all = (sm.vmask[g][i & 3][0] & sm.vmask[g][i & 3][1]) == 0xffffffffu;
       const int rows = a_tile ? box : PT_ROWS;        // rows per TMA box; box 0: pages that no box fits
       const bool tma = all && (a_tile ? !SPARSE && box > 0 : true);
       const uint32_t ph = (i & 1) ^ 1;
@@ -268,7 +261,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (!in_time) atomicExch(&sm.abort_flag, 1);
       // resolve the group's next tile while the copies are in flight
       step(2);
-      if (more) { resolve(); prefetch(); }
+      if (more) resolve();
       if (!tma) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         tc::fence_proxy_async_smem();
@@ -428,7 +421,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         const int st = i & 1;
         const uint32_t ph = (i >> 1) & 1;
         bool w = tc::mbar_wait(&sm.full[st][0], ph);  // the mask of the tile's rows
-        const uint32_t vm = sm.vmask[st][ph][half] >> (16 * wg);
+        const uint32_t vm = sm.vmask[st][(i >> 1) & 3][half] >> (16 * wg);
         w = w && tc::mbar_wait(&sm.sfull[st], ph);
         w = __all_sync(0xffffffffu, w && !*(volatile int*)&sm.abort_flag);
         if (!w) { ok = false; break; }
