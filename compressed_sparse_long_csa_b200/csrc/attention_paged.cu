@@ -177,26 +177,32 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
 // on the order in which the units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece, and
 // the latency of its few round trips.
 constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 8, PM_PER_SM = 3;
+// Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)
+constexpr size_t pm_unit_bytes(bool part16) { return PM_H * (sizeof(float4) + (part16 ? sizeof(float2) : 0)) + sizeof(int4); }
 template <typename T, bool PART16>
 __global__ void __launch_bounds__(PM_THREADS, PM_PER_SM)
 paged_merge_kernel(PagedAttnArgs a) {
   constexpr int V = PART16 ? 8 : 4;                  // dims of a 16-byte piece
-  extern __shared__ float4 wts[];                    // [piece][8] e^{m_p - M} times the quarters' powers, then the list
+  // per unit: the list {unit, sequence, partials, -}; per partial and head: {m, l, s0, s1}, then
+  // e^{m - M} times the quarters' powers, and {s2, s3}
+  extern __shared__ int4 list[];
+  float4* const wts = reinterpret_cast<float4*>(list + a.units);
+  float2* const s23 = reinterpret_cast<float2*>(wts + (size_t)a.units * PM_H);
   __shared__ float red[2][PM_THREADS / 32][PM_H];
   __shared__ float sums[V][PM_THREADS];
   __shared__ int count;
-  int* list = reinterpret_cast<int*>(wts + (size_t)a.units * PM_H);
   const int dv = a.dv, H = a.H;
   const int hl = threadIdx.x & (PM_H - 1), j = threadIdx.x / PM_H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int2* notes = paged_notes(a);
   if (warp == 0) {
+    const int2* notes = paged_notes(a);
     int n = 0;
+#pragma unroll 4
     for (int u0 = 0; u0 < a.units; u0 += 32) {
-      const bool cut = u0 + lane < a.units && __ldcg(&notes[u0 + lane]).y > 0;
-      const unsigned m = __ballot_sync(0xffffffffu, cut);
-      if (cut) list[n + __popc(m & ((1u << lane) - 1u))] = u0 + lane;
+      const int2 note = u0 + lane < a.units ? __ldcg(&notes[u0 + lane]) : make_int2(-1, 0);
+      const unsigned m = __ballot_sync(0xffffffffu, note.y > 0);
+      if (note.y > 0) list[n + __popc(m & ((1u << lane) - 1u))] = make_int4(u0 + lane, note.x, note.y, 0);
       n += __popc(m);
     }
     if (lane == 0) count = n;
@@ -209,33 +215,59 @@ paged_merge_kernel(PagedAttnArgs a) {
   int gw = PM_C;                                      // threads along a slice; the other PM_C / gw share its partials
   while (gw > 4 && gw / 2 >= width) gw >>= 1;
   const int groups = PM_C / gw, g = j / gw, jc = j - g * gw;
+  const size_t block = paged_part_block(H, dv);
   for (int item = blockIdx.x; item < count * hb * slices; item += gridDim.x) {
-    const int sl = item % slices, blk8 = item / slices % hb, unit = list[item / (slices * hb)];
-    const int2 note = __ldcg(&notes[unit]);
-    const int b = note.x, n = note.y, h = blk8 * PM_H + hl;
+    const int sl = item % slices, blk8 = item / slices % hb;
+    const int4 cut = list[item / (slices * hb)];
+    const int b = cut.y, n = cut.z, h = blk8 * PM_H + hl;
     const bool hv = h < H;
     const int hc = hv ? h : H - 1;
     // partial 0 lies in slot 1 of the unit, partial p > 0 in slot 0 of unit + p
-    const size_t block = paged_part_block(H, dv);
-    const float* part = a.part + (size_t)(2 * unit) * block;
+    const float* part = a.part + (size_t)(2 * cut.x) * block;
     auto partial = [&](int p) { return part + (p ? 2 * p * block : block); };
-    auto load = [&](int p, int c) {
-      return __ldcg(reinterpret_cast<const uint4*>(partial(p)) + (size_t)c * H + hc);
+    auto load = [&](int p, int c) { return __ldcg(reinterpret_cast<const uint4*>(partial(p)) + (size_t)c * H + hc); };
+    const size_t rec = paged_part_rec(H, dv, hc);
+    const float sk = a.sink[hc];
+    float acc[V];
+    auto add = [&](const uint4& v, float w) {
+      const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (PART16) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u4[q]));
+          acc[2 * q % V] = fmaf(w, f.x, acc[2 * q % V]);
+          acc[(2 * q + 1) % V] = fmaf(w, f.y, acc[(2 * q + 1) % V]);
+        } else {
+          acc[q] = fmaf(w, __uint_as_float(u4[q]), acc[q]);
+        }
+      }
     };
-    const int c0 = sl * width + jc, c1 = min(pieces, (sl + 1) * width);
+    auto store = [&](int c, float inv) {
+      T* dst = (T*)a.out + ((size_t)b * H + h) * dv + V * c;
+#pragma unroll
+      for (int u = 0; u < V; ++u) acc[u] *= inv;
+      if constexpr (V == Elem<T>::VEC) {
+        Elem<T>::st_vec(dst, acc);
+      } else {
+#pragma unroll
+        for (int u = 0; u < V; ++u) Elem<T>::st(dst + u, acc[u]);
+      }
+    };
+    const int cend = min(pieces, (sl + 1) * width);
+    const int c0 = sl * width + jc;
+    float M = sk;
+    for (int p = j; p < n; p += PM_C) {
+      const float4* r = reinterpret_cast<const float4*>(partial(p) + rec);
+      const float4 r0 = __ldcg(r);
+      if (PART16) s23[p * PM_H + hl] = __ldcg(reinterpret_cast<const float2*>(r + 1));
+      wts[p * PM_H + hl] = r0;
+      M = fmaxf(M, r0.x);
+    }
     // the group's first partials are on their way while the weights are formed
     uint4 x[PM_EARLY];
 #pragma unroll
     for (int u = 0; u < PM_EARLY; ++u)
-      if (g + u * groups < n && c0 < c1) x[u] = load(g + u * groups, c0);
-    const float sk = a.sink[hc];
-    const size_t rec = paged_part_rec(H, dv, hc);
-    float M = sk;
-    for (int p = j; p < n; p += PM_C) {
-      const float4 r = __ldcg(reinterpret_cast<const float4*>(partial(p) + rec));
-      wts[p * PM_H + hl] = r;
-      M = fmaxf(M, r.x);
-    }
+      if (g + u * groups < n && c0 < cend) x[u] = load(g + u * groups, c0);
 #pragma unroll
     for (int o = PM_H; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane < PM_H) red[0][warp][lane] = M;
@@ -244,15 +276,15 @@ paged_merge_kernel(PagedAttnArgs a) {
     for (int w = 0; w < PM_THREADS / 32; ++w) M = fmaxf(M, red[0][w][hl]);
     float den = 0.f;
     for (int p = j; p < n; p += PM_C) {
-      const float4 r = wts[p * PM_H + hl];            // {m, l, s0, s1}, this thread's own
+      const float4 r = wts[p * PM_H + hl];            // this thread's own
       const float w = r.x == -INFINITY ? 0.f : __expf(r.x - M);
       den += w * r.y;
-      float4 q = make_float4(w, w, w, w);
       if (PART16) {
-        const float2 s = __ldcg(reinterpret_cast<const float2*>(partial(p) + rec + 4));
-        q = make_float4(w * r.z, w * r.w, w * s.x, w * s.y);
+        const float2 s = s23[p * PM_H + hl];
+        wts[p * PM_H + hl] = make_float4(w * r.z, w * r.w, w * s.x, w * s.y);
+      } else {
+        wts[p * PM_H + hl].x = w;
       }
-      wts[p * PM_H + hl] = q;
     }
 #pragma unroll
     for (int o = PM_H; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -262,26 +294,11 @@ paged_merge_kernel(PagedAttnArgs a) {
 #pragma unroll
     for (int w = 0; w < PM_THREADS / 32; ++w) den += red[1][w][hl];
     const float inv = den > 0.f ? 1.f / den : 0.f;
-    for (int c = c0; c - jc < c1; c += gw) {
-      float acc[V];
+    for (int c = c0; c - jc < cend; c += gw) {
 #pragma unroll
       for (int u = 0; u < V; ++u) acc[u] = 0.f;
-      const float* wq = reinterpret_cast<const float*>(wts) + 4 * hl + (PART16 ? (c >> 4) & 3 : 0);   // 16 pieces a quarter
-      auto add = [&](const uint4& v, int p) {
-        const float w = wq[p * PM_H * 4];
-        const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (PART16) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u4[q]));
-            acc[2 * q % V] = fmaf(w, f.x, acc[2 * q % V]);
-            acc[(2 * q + 1) % V] = fmaf(w, f.y, acc[(2 * q + 1) % V]);
-          } else {
-            acc[q] = fmaf(w, __uint_as_float(u4[q]), acc[q]);
-          }
-        }
-      };
-      if (c < c1) {
+      const float* wq = reinterpret_cast<const float*>(wts + hl) + (PART16 ? (c >> 4) & 3 : 0);
+      if (c < cend) {
         if (c != c0) {
 #pragma unroll
           for (int u = 0; u < PM_EARLY; ++u)
@@ -289,9 +306,9 @@ paged_merge_kernel(PagedAttnArgs a) {
         }
 #pragma unroll
         for (int u = 0; u < PM_EARLY; ++u)
-          if (g + u * groups < n) add(x[u], g + u * groups);
+          if (g + u * groups < n) add(x[u], wq[(g + u * groups) * PM_H * 4]);
 #pragma unroll 8
-        for (int p = g + PM_EARLY * groups; p < n; p += groups) add(load(p, c), p);
+        for (int p = g + PM_EARLY * groups; p < n; p += groups) add(load(p, c), wq[p * PM_H * 4]);
       }
       if (groups > 1) {                               // (the slice is one round of its threads)
 #pragma unroll
@@ -301,17 +318,7 @@ paged_merge_kernel(PagedAttnArgs a) {
 #pragma unroll
           for (int u = 0; u < V; ++u) acc[u] += sums[u][threadIdx.x + o * gw * PM_H];
       }
-      if (g == 0 && c < c1 && hv) {
-        T* dst = (T*)a.out + ((size_t)b * H + h) * dv + V * c;
-#pragma unroll
-        for (int u = 0; u < V; ++u) acc[u] *= inv;
-        if constexpr (V == Elem<T>::VEC) {
-          Elem<T>::st_vec(dst, acc);
-        } else {
-#pragma unroll
-          for (int u = 0; u < V; ++u) Elem<T>::st(dst + u, acc[u]);
-        }
-      }
+      if (g == 0 && c < cend && hv) store(c, inv);
     }
     if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
     __syncthreads();                                  // the weights and sums are read
@@ -327,7 +334,7 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(most < grid ? most : grid));
   cfg.blockDim = dim3(PM_THREADS);
-  cfg.dynamicSmemBytes = (size_t)a.units * (PM_H * sizeof(float4) + sizeof(int));  // a sequence has at most `units` pieces
+  cfg.dynamicSmemBytes = (size_t)a.units * pm_unit_bytes(part16);            // a sequence has at most `units` partials
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the pieces first of all
@@ -347,7 +354,8 @@ int paged_units_cc(int B, int H, int64_t rows_max) {
 }
 
 cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
-  a.tile = PC_ROWS;
+  a.tile_log2 = 5;
+  static_assert(PC_ROWS == 1 << 5, "tile rows");
   a.min_tiles = PC_MIN_TILES;
   a.units = paged_units(a, paged_units_cc(a.B, a.H, paged_rows_max(a)));
   const int warps = a.H < PC_WARPS ? a.H : PC_WARPS;

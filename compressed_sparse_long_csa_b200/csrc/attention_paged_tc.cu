@@ -639,7 +639,8 @@ int paged_units_tc(int B, int H, int64_t rows_max) {
 
 cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
   const int halves = a.H > PT_HC ? 2 : 1;
-  a.tile = PT_ROWS;
+  a.tile_log2 = 6;
+  static_assert(PT_ROWS == 1 << 6, "tile rows");
   a.min_tiles = PT_MIN_TILES;
   a.units = paged_units(a, paged_units_tc(a.B, a.H, paged_rows_max(a)));
   // the largest of 64, 32, 16, 8 rows that divides the pages: every box lies in one page

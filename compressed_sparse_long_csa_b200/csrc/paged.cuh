@@ -42,7 +42,7 @@ struct PagedAttnArgs {
   float* lse;                 // [B, H] or null
   float* part;                // partials of split sequences: paged_slots(units) blocks
   int units;                  // work units (CTAs per head group)
-  int tile;                   // rows per tile of the schedule
+  int tile_log2;              // rows per tile of the schedule, as a power of two
   int min_tiles;              // least tiles of a unit
   unsigned* err;
 };
@@ -70,7 +70,8 @@ __device__ __forceinline__ int paged_rows_w(const PagedAttnArgs& a, int b) {
   return n < 0 ? 0 : (n > a.W ? a.W : n);
 }
 __device__ __forceinline__ int64_t paged_tiles(const PagedAttnArgs& a, int b) {
-  return ((int64_t)paged_rows_a(a, b) + a.tile - 1) / a.tile + (paged_rows_w(a, b) + a.tile - 1) / a.tile;
+  const int na = paged_rows_a(a, b), nw = paged_rows_w(a, b), up = (1 << a.tile_log2) - 1;
+  return (((int64_t)na + up) >> a.tile_log2) + ((nw + up) >> a.tile_log2);
 }
 
 struct PagedPlan {
@@ -188,7 +189,8 @@ inline int paged_units(int ctas, int B, int64_t rows_max, int tile, int min_tile
 // The launch knows entries and window apart: at most this many units of the above are of use.
 inline int paged_units(const PagedAttnArgs& a, int units) {
   const int64_t rows = a.idx ? (int64_t)a.k : paged_capacity(a);
-  const int64_t tiles = a.B * ((rows + a.tile - 1) / a.tile + (a.W + a.tile - 1) / a.tile);
+  const int up = (1 << a.tile_log2) - 1;
+  const int64_t tiles = a.B * (((rows + up) >> a.tile_log2) + ((a.W + up) >> a.tile_log2));
   const int64_t u = (tiles + a.min_tiles - 1) / a.min_tiles;
   return (int)(u < units ? (u < 1 ? 1 : u) : units);
 }
