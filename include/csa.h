@@ -520,7 +520,7 @@ csa_status sparse_attn_decode_noalloc(const void* q, const void* cache, const in
  *            its last d_r values rotated
  *   seq      device [T] int32, or NULL: row t belongs to sequence t (T <= B)
  *   entry    device [T] int32; a negative entry marks a padding row: nothing of the token is
- *            read or written
+ *            written
  *   pos      device [T] int32 rotation positions, or NULL: the position is entry[t]
  *   inv_freq device [d_r / 2] fp32 frequencies (radians per position), or NULL with
  *            d_r = 0: no rotation.  The angle pos * inv_freq is formed in fp64.
