@@ -21,27 +21,45 @@ namespace {
 constexpr int PC_ROWS = 32;      // rows per tile: one lane per row in the logits
 constexpr int PC_WARPS = 8;      // heads per CTA: one warp each
 constexpr int PC_MAXD = 576;
-constexpr int PC_MIN_TILES = 2;
+constexpr int PC_MIN_TILES = 1;
 
-// grid (units, ceil(H / 8)); shared memory [32][dk + 4] rows and [8][dk] queries, fp32.
-// Logits: lane r of a head's warp forms the whole dot product of row r (no reduction
-// across lanes); the pitch dk + 4 spreads the lanes' 16-byte loads over the banks.
-// Values: lane i owns dims 4i .. 4i+3 (+128 j).
+__device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool zero) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(zero ? 0 : 16) : "memory");
+}
+
+template <typename T> __device__ __forceinline__ void load4(const T* p, float* x);
+template <> __device__ __forceinline__ void load4<float>(const float* p, float* x) { Elem<float>::ld_vec(p, x); }
+template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(v.x << 16);
+  x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16);
+  x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+// grid (units, ceil(H / 8)); shared memory: `bufs` (1 or 2) tiles of 32 rows as stored, each row
+// 16 bytes apart from the next, and the warps' queries in fp32.  Lane r of every warp knows row r
+// of a tile; a tile is copied by 16-byte cp.async while the one before is worked on (two buffers)
+// and its rows are looked up a tile earlier still.
+// Logits: lane r of a head's warp forms the whole dot product of row r (no reduction across
+// lanes); the pitch spreads the lanes' 16-byte loads over the banks.  Values: lane i owns dims
+// 4i .. 4i+3 (+128 j).
+// Bound: latency for few rows (about 5 us: lengths, table, rows, one tile's work, the store), the
+// fp32 pipe and shared memory (two 16-byte loads for 4 or 8 products) for many.
 template <typename T>
 __global__ void __launch_bounds__(PC_WARPS * 32)
-paged_attn_cc_kernel(PagedAttnArgs a) {
-  extern __shared__ float4 smem4[];
+paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
+  extern __shared__ uint4 smem16[];
   __shared__ int64_t scratch[66];
-  __shared__ int64_t rowi[PC_ROWS];                  // row of the pool, -1 = none
+  constexpr int VEC = Elem<T>::VEC;
   const int unit = blockIdx.x, hg = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
-  const int dk = a.dk, dv = a.dv, pitch = dk + 4;
-  float* Ks = reinterpret_cast<float*>(smem4);
-  float* Qs = Ks + PC_ROWS * pitch + (size_t)warp * dk;
+  const int dk = a.dk, dv = a.dv, pitch = dk + VEC, vecs = dk / VEC;
+  T* const tiles_s = reinterpret_cast<T*>(smem16);
+  float* const Qs = reinterpret_cast<float*>(tiles_s + (size_t)bufs * PC_ROWS * pitch) + (size_t)warp * dk;
   const int h = hg * PC_WARPS + warp;
   const bool hv = h < a.H;
-  constexpr int VEC = Elem<T>::VEC;
-  const int vecs = dk / VEC;
   constexpr int NO = (PC_MAXD + 127) / 128;          // groups of 4 dims per lane
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // the merge waits for this grid itself
@@ -64,6 +82,26 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
     const bool whole = t == 0 && t1 == tiles;
     const int slot = 2 * unit + (t == 0 ? 1 : 0);
     left -= t1 - t;
+    // the lane's row of a tile: in the pool or the window, -1 = none
+    auto resolve = [&](int64_t tile) {
+      if (tile >= t1) return -1;
+      const bool in_a = tile < ta;
+      const int64_t v = (in_a ? tile : tile - ta) * PC_ROWS + lane;
+      if (in_a) return v < na ? (int)paged_row(a, b, (int)v) : -1;
+      return v < nw ? (int)((int64_t)b * a.W + v) : -1;
+    };
+    auto copy = [&](int64_t tile, int row, int buf) {
+      const T* base = tile < ta ? (const T*)a.pages : (const T*)a.win;
+      T* dst = tiles_s + (size_t)buf * PC_ROWS * pitch;
+      for (int i = threadIdx.x; i < PC_ROWS * vecs; i += threads) {       // whole warps
+        const int r = i / vecs, c = (i - r * vecs) * VEC;
+        const int y = __shfl_sync(0xffffffffu, row, r);
+        cp_async16_zfill(dst + r * pitch + c, base + (size_t)(y < 0 ? 0 : y) * dk + c, y < 0);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int row = resolve(t), next = resolve(t + 1);
+    copy(t, row, 0);
     if (hv)
       for (int c = lane * VEC; c < dk; c += 32 * VEC) {
         float x[VEC];
@@ -75,61 +113,63 @@ paged_attn_cc_kernel(PagedAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < NO; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     float m_run = -INFINITY, l_run = 0.f;
+    int buf = 0;
     for (; t < t1; ++t) {
-      __syncthreads();                                // the tile before is no longer read
-      const bool in_a = t < ta;
-      const int64_t v0 = (in_a ? t : t - ta) * PC_ROWS;
-      if (threadIdx.x < PC_ROWS) {
-        const int64_t v = v0 + threadIdx.x;
-        rowi[threadIdx.x] = in_a ? (v < na ? paged_row(a, b, (int)v) : -1) : (v < nw ? (int64_t)b * a.W + v : -1);
-      }
+      const bool ahead = bufs == 2 && t + 1 < t1;
+      if (ahead) copy(t + 1, next, buf ^ 1);
+      const int after = resolve(t + 2);                // its loads are in flight during the tile's work
+      if (ahead) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-      const T* base = in_a ? (const T*)a.pages : (const T*)a.win;
-      for (int i = threadIdx.x; i < PC_ROWS * vecs; i += threads) {
-        const int r = i / vecs, c = (i - r * vecs) * VEC;
-        float x[VEC];
-#pragma unroll
-        for (int u = 0; u < VEC; ++u) x[u] = 0.f;
-        if (rowi[r] >= 0) Elem<T>::ld_vec(base + (size_t)rowi[r] * dk + c, x);
-#pragma unroll
-        for (int u = 0; u < VEC; u += 4)
-          *reinterpret_cast<float4*>(Ks + r * pitch + c + u) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
-      }
-      __syncthreads();
-      if (!hv) continue;
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-      const float* kr = Ks + lane * pitch;
+      const T* Ks = tiles_s + (size_t)buf * PC_ROWS * pitch;
+      if (hv) {
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        const T* kr = Ks + lane * pitch;
 #pragma unroll 4
-      for (int c = 0; c < dk; c += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(kr + c), y = *reinterpret_cast<const float4*>(Qs + c);
-        s0 = fmaf(x.x, y.x, s0);
-        s1 = fmaf(x.y, y.y, s1);
-        s2 = fmaf(x.z, y.z, s2);
-        s3 = fmaf(x.w, y.w, s3);
-      }
-      const float logit = rowi[lane] >= 0 ? ((s0 + s1) + (s2 + s3)) * a.sm_scale : -INFINITY;
-      const float m_new = fmaxf(m_run, warp_max(logit));
-      if (m_new == -INFINITY) continue;               // no row of the piece so far
-      const float alpha = __expf(m_run - m_new);
-      const float p = __expf(logit - m_new);
-      l_run = l_run * alpha + warp_sum(p);
-      m_run = m_new;
+        for (int c = 0; c < dk; c += VEC) {
+          float x[VEC];
+          Elem<T>::ld_vec(kr + c, x);
 #pragma unroll
-      for (int i = 0; i < NO; ++i) { o[i].x *= alpha; o[i].y *= alpha; o[i].z *= alpha; o[i].w *= alpha; }
-      for (int r = 0; r < PC_ROWS; ++r) {
-        const float pr = __shfl_sync(0xffffffffu, p, r);
-        const float* vr = Ks + r * pitch + 4 * lane;
+          for (int u = 0; u < VEC; u += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(Qs + c + u);
+            s0 = fmaf(x[u], y.x, s0);
+            s1 = fmaf(x[u + 1], y.y, s1);
+            s2 = fmaf(x[u + 2], y.z, s2);
+            s3 = fmaf(x[u + 3], y.w, s3);
+          }
+        }
+        const float logit = row >= 0 ? ((s0 + s1) + (s2 + s3)) * a.sm_scale : -INFINITY;
+        const float m_new = fmaxf(m_run, warp_max(logit));
+        if (m_new != -INFINITY) {                      // else: no row of the piece so far
+          const float alpha = __expf(m_run - m_new);
+          const float p = __expf(logit - m_new);
+          l_run = l_run * alpha + warp_sum(p);
+          m_run = m_new;
 #pragma unroll
-        for (int i = 0; i < NO; ++i) {
-          if (4 * lane + 128 * i < dv) {
-            const float4 x = *reinterpret_cast<const float4*>(vr + 128 * i);
-            o[i].x = fmaf(pr, x.x, o[i].x);
-            o[i].y = fmaf(pr, x.y, o[i].y);
-            o[i].z = fmaf(pr, x.z, o[i].z);
-            o[i].w = fmaf(pr, x.w, o[i].w);
+          for (int i = 0; i < NO; ++i) { o[i].x *= alpha; o[i].y *= alpha; o[i].z *= alpha; o[i].w *= alpha; }
+#pragma unroll 4
+          for (int r = 0; r < PC_ROWS; ++r) {
+            const float pr = __shfl_sync(0xffffffffu, p, r);
+            const T* vr = Ks + r * pitch + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) {
+              if (4 * lane + 128 * i < dv) {
+                float x[4];
+                load4<T>(vr + 128 * i, x);
+                o[i].x = fmaf(pr, x[0], o[i].x);
+                o[i].y = fmaf(pr, x[1], o[i].y);
+                o[i].z = fmaf(pr, x[2], o[i].z);
+                o[i].w = fmaf(pr, x[3], o[i].w);
+              }
+            }
           }
         }
       }
+      __syncthreads();                                // the buffer is read
+      row = next;
+      next = after;
+      if (bufs == 2) buf ^= 1;
+      else if (t + 1 < t1) copy(t + 1, row, 0);
     }
     if (!hv) continue;
     if (whole) {
@@ -359,15 +399,16 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
   a.min_tiles = PC_MIN_TILES;
   a.units = paged_units(a, paged_units_cc(a.B, a.H, paged_rows_max(a)));
   const int warps = a.H < PC_WARPS ? a.H : PC_WARPS;
-  const size_t smem = ((size_t)PC_ROWS * (a.dk + 4) + (size_t)warps * a.dk) * sizeof(float);
-  dim3 grid(a.units, (a.H + PC_WARPS - 1) / PC_WARPS);
   auto go = [&](auto tag) {
     using T = decltype(tag);
+    const size_t tile = (size_t)PC_ROWS * (a.dk + Elem<T>::VEC) * sizeof(T), qs = (size_t)warps * a.dk * sizeof(float);
+    const int bufs = 2 * tile + qs <= 48 * 1024 ? 2 : 1;      // two only while several CTAs still share an SM
+    const dim3 grid(a.units, (a.H + PC_WARPS - 1) / PC_WARPS);
     static std::atomic<uint64_t> ready;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(paged_attn_cc_kernel<T>), ready, 96 * 1024);
     if (e != cudaSuccess) return e;
     note_launch();
-    paged_attn_cc_kernel<T><<<grid, warps * 32, smem, st>>>(a);
+    paged_attn_cc_kernel<T><<<grid, warps * 32, bufs * tile + qs, st>>>(a, bufs);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_paged_merge(a, dtype, false, st);
