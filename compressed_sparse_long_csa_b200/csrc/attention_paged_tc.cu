@@ -259,9 +259,6 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         ++n_hi;
       }
       if (!in_time) atomicExch(&sm.abort_flag, 1);
-      // resolve the group's next tile while the copies are in flight
-      step(2);
-      if (more) resolve();
       if (!tma) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         tc::fence_proxy_async_smem();
@@ -272,6 +269,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         named_bar(1 + g, PT_GROUP);
         if (lg == 0) tc::mbar_arrive(&sm.full[g][1]);
       }
+      // the next tile's rows, looked up while this one is worked on
+      step(2);
+      if (more) resolve();
     }
     cp_async_wait_all();
     // drain: no TMA write of this CTA may be in flight when the CTA exits
