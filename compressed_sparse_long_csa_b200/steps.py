@@ -10,6 +10,9 @@ A *step* is what one attention layer does for one batch:
 * CSA prefill chunk: csa_compress (the chunk's entries) -> lightning_index (per
   query eligibility) -> sparse_attn_prefill.
 * Hybrid pair: a CSA decode step then an HCA decode step.
+* Paged decode: after ``page_caches`` the decode steps keep the compressed entries in pages:
+  the entry is pooled into a row of its own, latent_append_paged stores it in its page, and
+  the attention is the paged call.  The indexer's keys stay contiguous.
 
 The functions take a dict of device tensors (see ``upload``) and only issue the
 calls; every number is computed by the library's kernels.
@@ -77,6 +80,46 @@ def _ifmt(D):
     return {"f32": N.CSA_IFMT_F32, "e4m3": N.CSA_IFMT_E4M3, "mxfp4": N.CSA_IFMT_MXFP4}[D["ifmt"]]
 
 
+def page_caches(T, D, kind, page_size=64):
+    """Move the entry caches of an uploaded decode workload into pages.  T gets, per cache, the pool
+    "pages" and its "block_table" (room for the contiguous cache's entries), the rows "fresh" that a
+    step pools its entry into, where these go ("fresh_seq", "fresh_entry") and the workspace of the
+    paged attention.  The decode steps then use these; the contiguous cache is left alone."""
+    for p, csa in (("", kind != "hca_decode"), ("h_", False)):
+        if p + "cache" not in T:
+            continue
+        cache, entry0 = T[p + "cache"], T[p + "entry0"]
+        B, n_max, d = cache.shape
+        i32 = dict(dtype=torch.int32, device=cache.device)
+        width = -(-n_max // page_size)
+        pages = torch.zeros(B * width, page_size, d, dtype=cache.dtype, device=cache.device)
+        pages.view(B, width * page_size, d)[:, :n_max] = cache
+        T[p + "pages"] = pages
+        T[p + "block_table"] = torch.arange(B * width, **i32).view(B, width)
+        rows = 2 if csa else 1
+        T[p + "fresh"] = torch.zeros(B, rows, d, dtype=cache.dtype, device=cache.device)
+        T[p + "fresh_seq"] = torch.arange(B, **i32).repeat_interleave(rows)
+        if csa:
+            # the CSA pooling takes its entry's index from where it writes (entry 0 has no block
+            # before it): row 0 for a sequence's first entry, row 1 for any other; the row that
+            # is not written is no entry of the cache (-1)
+            first = entry0 == 0
+            T[p + "fresh0"] = entry0.clamp(max=1)
+            T[p + "fresh_entry"] = torch.stack((torch.where(first, 0, -1), torch.where(first, -1, entry0)), 1).to(torch.int32).view(-1)
+        else:
+            T[p + "fresh0"] = torch.zeros(B, **i32)
+            T[p + "fresh_entry"] = entry0.clone()
+        attended = (D["k"] if csa else width * page_size) + D["W"]
+        T[p + "paws"] = torch.empty(N.attn_decode_paged_workspace_size(B, D["H"], D["dv"], attended), dtype=torch.uint8,
+                                    device=cache.device)
+
+
+def _append_fresh(T, p, stream):
+    fresh = T[p + "fresh"]
+    N.latent_append_paged(fresh.view(-1, fresh.shape[2]), T[p + "fresh_entry"], T[p + "pages"], T[p + "block_table"],
+                          seq=T[p + "fresh_seq"], stream=stream)
+
+
 _SIDE = {}
 
 
@@ -127,7 +170,25 @@ def _csa_layer(T, D, stream, attend):
     attend(main)
 
 
+def _csa_decode_paged_step(T, D, stream):
+    """csa_decode_step with the entries in pages (page_caches)."""
+    N.csa_compress(T["Ca"], T["Cb"], T["Za"], T["Zb"], T["Ba"], T["Bb"], T["prev_Cb"], T["prev_Zb"], T["fresh0"],
+                   T["fresh"], m=D["m"], stream=stream)
+    _append_fresh(T, "", stream)
+    if "CaI" in T:
+        N.index_key_compress(T["CaI"], T["CbI"], T["ZaI"], T["ZbI"], T["BaI"], T["BbI"], T["prev_CbI"], T["prev_ZbI"],
+                             T["entry0"], T["kI"], T["kI_scale"], _ifmt(D), m=D["m"], stream=stream)
+        N.window_append(T["raw_new"], T["win"], T["win_slot"], stream=stream)
+    N.lightning_index(T["qI"], T.get("qI_scale"), T["w"], T["kI"], T.get("kI_scale"), T["n_entries"], T["q_pos"],
+                      D["k"], _ifmt(D), T["idx"], T["iws"], m=D["m"], stream=stream)
+    N.sparse_attn_decode_paged(T["q"][:, 0], T["pages"], T["block_table"], T["idx"][:, 0], T["win"], T["win_len"],
+                               T["sink"], D["sm_scale"], D["dv"], T["out"][:, 0], T["lse"][:, 0], T["paws"], stream=stream)
+
+
 def csa_decode_step(T, D, stream=None):
+    if "pages" in T:
+        _csa_decode_paged_step(T, D, stream)
+        return
     _csa_layer(T, D, stream, lambda st: N.sparse_attn_decode(
         T["q"][:, 0], T["cache"], T["idx"][:, 0], T["win"], T["win_len"], T["sink"], D["sm_scale"], D["dv"],
         T["out"][:, 0], T["lse"][:, 0], T["aws"], stream=st))
@@ -140,6 +201,14 @@ def hca_decode_step(T, D, stream=None, prefix=""):
     p = prefix
     if p + "raw_new" in T:
         N.window_append(T[p + "raw_new"], T[p + "win"], T["win_slot"], stream=stream)
+    if p + "pages" in T:
+        N.hca_compress(T[p + "C"], T[p + "Z"], T[p + "bias"], T[p + "fresh0"], T[p + "fresh"], m_prime=D["m_prime"],
+                       stream=stream)
+        _append_fresh(T, p, stream)
+        N.hca_attn_decode_paged(T[p + "q"][:, 0], T[p + "pages"], T[p + "block_table"], T[p + "n_entries"], T[p + "win"],
+                                T[p + "win_len"], T[p + "sink"], D["sm_scale"], D["dv"], T[p + "out"][:, 0],
+                                T[p + "lse"][:, 0], T[p + "paws"], stream=stream)
+        return
     N.hca_compress_attn_decode(T[p + "C"], T[p + "Z"], T[p + "bias"], T[p + "entry0"], T[p + "q"][:, 0],
                                T[p + "cache"], T[p + "n_entries"], T[p + "win"], T[p + "win_len"], T[p + "sink"],
                                D["sm_scale"], D["dv"], T[p + "out"][:, 0], T[p + "lse"][:, 0], T[p + "aws"],
