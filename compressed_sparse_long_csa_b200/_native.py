@@ -321,30 +321,28 @@ def sparse_attn_decode_noalloc(q, cache, idx, win, win_len, sink, sm_scale, d_v,
 
 # ---- paged cache.  The tensors' shapes, types, strides and device are checked here (the C
 # calls see addresses only): what does not fit raises CsaError and nothing is launched.  A
-# decode step makes these calls once per layer, so the checks are kept to a few plain
-# comparisons a tensor; the message is made when one fails.
+# decode step makes these calls once per layer and waits for nothing else on the host, so the
+# checks are plain comparisons, written out (a helper per tensor cost 2 us a call); the message
+# is made when one fails.
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_device_now = torch.cuda.current_device
+_stream_now = torch._C._cuda_getCurrentRawStream
 
 
-def _unfit(name, what, want):
-    raise CsaError(f"{name}: {what} must be {want}")
-
-
-def _want(name, what, t, dtype, shape, di):
-    if t.dtype != dtype or t.shape != shape or t.get_device() != di or not t.is_contiguous():
-        _unfit(name, what, f"a contiguous {dtype} tensor of shape {tuple(shape)} on the pages' device, got {t.dtype} "
-                           f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
+def _unfit(name, what, t, want):
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
+    raise CsaError(f"{name}: {what} must be {want} on the pages' device, got {got}")
 
 
 def _paged(name, pages, block_table):
     """Checks of the pool and its table; the device's index."""
     di = pages.get_device()
-    if di < 0 or di != torch.cuda.current_device():
-        _unfit(name, "pages", f"on the current CUDA device, got {pages.device}")
+    if di < 0 or di != _device_now():
+        raise CsaError(f"{name}: pages must be on the current CUDA device, got {pages.device}")
     if pages.dim() != 3 or not pages.is_contiguous() or (pages.dtype != _BF16 and pages.dtype != _F32):
-        _unfit(name, "pages", "a contiguous bf16 or fp32 tensor [n_pages, page_size, d]")
+        _unfit(name, "pages", pages, "a contiguous bf16 or fp32 tensor [n_pages, page_size, d]")
     if block_table.dim() != 2 or block_table.dtype != _I32 or block_table.get_device() != di or not block_table.is_contiguous():
-        _unfit(name, "block_table", "a contiguous int32 tensor [B, table_width] on the pages' device")
+        _unfit(name, "block_table", block_table, "a contiguous int32 tensor [B, table_width]")
     return di
 
 
@@ -359,40 +357,42 @@ def latent_append_paged(rows, entry, pages, block_table, seq=None, pos=None, inv
     n_pages, page, d = pages.shape
     B, width = block_table.shape
     dt = pages.dtype
-    if entry.dim() != 1:
-        _unfit(name, "entry", "an int32 tensor [T]")
-    T = entry.shape[0]
-    of_T = (T,)
-    _want(name, "entry", entry, _I32, of_T, di)
+    if entry.dim() != 1 or entry.dtype != _I32 or entry.get_device() != di or not entry.is_contiguous():
+        _unfit(name, "entry", entry, "a contiguous int32 tensor [T]")
+    of_T = entry.shape
+    T = of_T[0]
     if rows.shape != (T, d) or rows.dtype != dt or rows.get_device() != di or (d > 1 and rows.stride(1) != 1):
-        _unfit(name, "rows", f"[{T}, {d}] {dt} on the pages' device with a dense last dimension")
-    ld = rows.stride(0) if T > 1 else d
-    sp = pp = fp = qp = qo = None
-    d_r = H = d_q = ld_t = ld_h = 0
+        _unfit(name, "rows", rows, f"[{T}, {d}] {dt} with a dense last dimension")
+    sp = pp = fp = qp = qo = d_r = H = d_q = ld_t = ld_h = 0
     if seq is not None:
-        _want(name, "seq", seq, _I32, of_T, di)
+        if seq.dtype != _I32 or seq.shape != of_T or seq.get_device() != di or not seq.is_contiguous():
+            _unfit(name, "seq", seq, f"a contiguous int32 tensor [{T}]")
         sp = seq.data_ptr()
     if pos is not None:
-        _want(name, "pos", pos, _I32, of_T, di)
+        if pos.dtype != _I32 or pos.shape != of_T or pos.get_device() != di or not pos.is_contiguous():
+            _unfit(name, "pos", pos, f"a contiguous int32 tensor [{T}]")
         pp = pos.data_ptr()
     if inv_freq is not None:
-        d_r = 2 * inv_freq.numel()
-        _want(name, "inv_freq", inv_freq, _F32, (d_r // 2,), di)
+        if inv_freq.dim() != 1 or inv_freq.dtype != _F32 or inv_freq.get_device() != di or not inv_freq.is_contiguous():
+            _unfit(name, "inv_freq", inv_freq, "a contiguous fp32 tensor [d_r / 2]")
+        d_r = 2 * inv_freq.shape[0]
         fp = inv_freq.data_ptr()
-    if (q is None) != (q_pe is None):
-        _unfit(name, "q", "given together with q_pe")
-    if q is not None:
-        if q.dim() != 3:
-            _unfit(name, "q", "[T, H, d_q]")
+    if q is not None and q_pe is not None:
+        if q.dim() != 3 or q.dtype != dt or q.shape[0] != T or q.get_device() != di or not q.is_contiguous():
+            _unfit(name, "q", q, f"a contiguous {dt} tensor [{T}, H, d_q]")
         _, H, d_q = q.shape
-        _want(name, "q", q, dt, (T, H, d_q), di)
         if q_pe.shape != (T, H, d_r) or q_pe.dtype != dt or q_pe.get_device() != di or q_pe.stride(2) != 1:
-            _unfit(name, "q_pe", f"[{T}, {H}, {d_r}] {dt} on the pages' device with a dense last dimension")
+            _unfit(name, "q_pe", q_pe, f"[{T}, {H}, {d_r}] {dt} with a dense last dimension")
         ld_t, ld_h, _ = q_pe.stride()
         qp, qo = q_pe.data_ptr(), q.data_ptr()
-    _check(lib.latent_append_paged(rows.data_ptr(), ld, sp, entry.data_ptr(), pp, fp, d_r, 1 if interleaved else 0,
-                                   pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, B, T, d, qp, ld_t, ld_h,
-                                   qo, H, d_q, CSA_BF16 if dt == _BF16 else CSA_F32, _stream(stream)), name)
+    elif q is not None or q_pe is not None:
+        raise CsaError(f"{name}: q and q_pe come together")
+    st = lib.latent_append_paged(rows.data_ptr(), rows.stride(0) if T > 1 else d, sp, entry.data_ptr(), pp, fp, d_r,
+                                 1 if interleaved else 0, pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, B,
+                                 T, d, qp, ld_t, ld_h, qo, H, d_q, CSA_BF16 if dt == _BF16 else CSA_F32,
+                                 _stream_now(di) if stream is None else _stream(stream))
+    if st:
+        _check(st, name)
 
 
 def attn_decode_paged_workspace_size(B, H, d_v, rows_max):
@@ -404,37 +404,39 @@ def _paged_attn(name, call, q, pages, block_table, sel, sparse, win, win_len, si
     n_pages, page, d_k = pages.shape
     B, width = block_table.shape
     dt = pages.dtype
-    if q.dim() != 3:
-        _unfit(name, "q", "[B, H, d_k]")
+    if q.dim() != 3 or q.dtype != dt or q.shape[0] != B or q.shape[2] != d_k or q.get_device() != di or not q.is_contiguous():
+        _unfit(name, "q", q, f"a contiguous {dt} tensor [{B}, H, {d_k}]")
     H = q.shape[1]
-    _want(name, "q", q, dt, (B, H, d_k), di)
-    _want(name, "out", out, dt, (B, H, d_v), di)
-    _want(name, "sink", sink, _F32, (H,), di)
+    if out.dtype != dt or out.shape != (B, H, d_v) or out.get_device() != di or not out.is_contiguous():
+        _unfit(name, "out", out, f"a contiguous {dt} tensor [{B}, {H}, {d_v}]")
+    if sink.dtype != _F32 or sink.shape != (H,) or sink.get_device() != di or not sink.is_contiguous():
+        _unfit(name, "sink", sink, f"a contiguous fp32 tensor [{H}]")
     if sparse:
-        if sel.dim() != 2:
-            _unfit(name, "idx", "[B, k]")
-        k = sel.shape[1]
-        _want(name, "idx", sel, _I32, (B, k), di)
-        picked = (sel.data_ptr(), k)
+        if sel.dim() != 2 or sel.dtype != _I32 or sel.shape[0] != B or sel.get_device() != di or not sel.is_contiguous():
+            _unfit(name, "idx", sel, f"a contiguous int32 tensor [{B}, k]")
+        picked = (sel.data_ptr(), sel.shape[1])
     else:
-        _want(name, "n_entries", sel, _I32, (B,), di)
+        if sel.dtype != _I32 or sel.shape != (B,) or sel.get_device() != di or not sel.is_contiguous():
+            _unfit(name, "n_entries", sel, f"a contiguous int32 tensor [{B}]")
         picked = (sel.data_ptr(),)
-    W, wp, lp, ep = 0, None, None, None
+    W = wp = lp = ep = 0
     if win is not None:
-        if win.dim() != 3 or win_len is None:
-            _unfit(name, "win", "[B, W, d_k] with win_len")
-        W = win.shape[1]
-        _want(name, "win", win, dt, (B, W, d_k), di)
-        _want(name, "win_len", win_len, _I32, (B,), di)
-        wp, lp = win.data_ptr(), win_len.data_ptr()
+        if win.dim() != 3 or win.dtype != dt or win.shape[0] != B or win.shape[2] != d_k or win.get_device() != di or not win.is_contiguous():
+            _unfit(name, "win", win, f"a contiguous {dt} tensor [{B}, W, {d_k}]")
+        if win_len is None or win_len.dtype != _I32 or win_len.shape != (B,) or win_len.get_device() != di or not win_len.is_contiguous():
+            _unfit(name, "win_len", win_len, f"a contiguous int32 tensor [{B}]")
+        W, wp, lp = win.shape[1], win.data_ptr(), win_len.data_ptr()
     if lse is not None:
-        _want(name, "lse", lse, _F32, (B, H), di)
+        if lse.dtype != _F32 or lse.shape != (B, H) or lse.get_device() != di or not lse.is_contiguous():
+            _unfit(name, "lse", lse, f"a contiguous fp32 tensor [{B}, {H}]")
         ep = lse.data_ptr()
     if workspace is None or workspace.get_device() != di or not workspace.is_contiguous():
-        _unfit(name, "workspace", "a contiguous tensor on the pages' device")
-    _check(call(q.data_ptr(), pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, *picked, wp, lp,
-                sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, CSA_BF16 if dt == _BF16 else CSA_F32, out.data_ptr(), ep,
-                workspace.data_ptr(), workspace.nbytes, _stream(stream)), name)
+        _unfit(name, "workspace", workspace, "a contiguous tensor")
+    st = call(q.data_ptr(), pages.data_ptr(), n_pages, page, block_table.data_ptr(), width, *picked, wp, lp,
+              sink.data_ptr(), B, H, d_k, d_v, W, sm_scale, CSA_BF16 if dt == _BF16 else CSA_F32, out.data_ptr(), ep,
+              workspace.data_ptr(), workspace.nbytes, _stream_now(di) if stream is None else _stream(stream))
+    if st:
+        _check(st, name)
 
 
 def hca_attn_decode_paged(q, pages, block_table, n_entries, win, win_len, sink, sm_scale, d_v, out, lse=None,
