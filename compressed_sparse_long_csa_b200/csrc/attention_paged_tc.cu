@@ -5,9 +5,10 @@
 // 64 heads (the MMA M) and one unit of the schedule (paged.cuh): a run of tiles that may span
 // several sequences ("segments").  Per tile:
 //   1. a loader group brings the 64 rows into its stage of a two-stage ring, in 128-byte
-//      swizzle atoms: runs of pages as TMA boxes of gcd(page, 64) rows, other rows (selected
-//      entries, partial tiles, pages that share no factor of 8 with 64) as 16-byte cp.async
-//      with the absent rows zeroed (P = 0 there, and 0 * NaN must not reach the sums);
+//      swizzle atoms: runs of pages as TMA boxes of gcd(page, 64) rows, scattered rows (selected
+//      entries, pages that share no factor of 8 with 64) by tile::gather4, tiles with absent rows
+//      by 16-byte cp.async with those rows zeroed (P = 0 there, and 0 * NaN must not reach the
+//      sums);
 //   2. one warp issues S = Q K^T (N = 64, 36 steps of K = 16) into TMEM;
 //   3. eight softmax warps read S, agree on the running maximum and write P to shared memory
 //      as two bf16 parts, P_hi = bf16(P) and P_lo = bf16(P - P_hi) (the second into the
@@ -49,7 +50,7 @@ struct PtSmem {
   uint8_t kv[2][PT_ATOMS][ATOM];             // 144 KB
   uint8_t p[PT_HC * 128];                    // P_hi: 64 heads x 64 rows bf16; between segments the row sums
   float smax[2][2][128];                     // per tile parity and warpgroup: the lanes' tile maxima
-  int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
+  alignas(16) int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
   uint32_t vmask[2][4][2];                   // per stage and use of it mod 4 (a group's warps may be a tile apart, the
                                              // softmax another behind): bit j of word j / 32 set when row j is valid
   uint64_t full[2][2], empty[2][2];          // per stage and half of the dims (0-255, 256-575)
@@ -66,6 +67,7 @@ struct PtMaps {
   CUtensorMap q;       // [B * H rows, 576], box 64 x 64
   CUtensorMap pages;   // [n_pages * page rows, 576], box 64 dims x box rows
   CUtensorMap win;     // [B * W rows, 576], box 64 x 64
+  CUtensorMap rows;    // the pages again, box 64 dims x 1 row (tile::gather4)
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // bytes < 16: zero-filled
@@ -235,6 +237,25 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
           }
         }
         __syncwarp();
+      } else if (all) {
+        // 64 scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp
+        // starts 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the
+        // issue slots and shared-memory ports that the softmax uses).
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
+          in_time = tc::mbar_wait(&sm.empty[g][x], ph) && in_time;
+          if (!in_time) break;
+          if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[g][x], (at1 - at0) * ATOM);
+          for (int p = (lg & 31) * (PT_GROUP / 32) + (lg >> 5); p < (at1 - at0) * (PT_ROWS / 4); p += PT_GROUP) {
+            const int quad = p & (PT_ROWS / 4 - 1), at = at0 + p / (PT_ROWS / 4);
+            const int4 r = *reinterpret_cast<const int4*>(&sm.rowy[g][4 * quad]);
+            tc::tma_gather4(sm.kv[g][at] + quad * 512, &maps.rows, &sm.full[g][x], 64 * at, r);
+          }
+          if (x) ++n_hi; else ++n_lo;
+        }
+        __syncwarp();
+        named_bar(1 + g, PT_GROUP);                   // the rows are read
       } else {
         const uint8_t* base = reinterpret_cast<const uint8_t*>(a_tile ? a.pages : a.win);
         const uint32_t kv0 = tc::smem_u32(sm.kv[g][0]);
@@ -259,7 +280,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         ++n_hi;
       }
       if (!in_time) atomicExch(&sm.abort_flag, 1);
-      if (!tma) {
+      if (!tma && !all) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         tc::fence_proxy_async_smem();
         named_bar(1 + g, PT_GROUP);
@@ -290,6 +311,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       tc::prefetch_tmap(&maps.q);
       tc::prefetch_tmap(&maps.pages);
       tc::prefetch_tmap(&maps.win);
+      tc::prefetch_tmap(&maps.rows);
     }
     bool ok = true;
     int n = 0, i = 0;
@@ -650,6 +672,7 @@ cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
   PtMaps maps;
   if (!row_map(&maps.q, a.q, (uint64_t)a.B * a.H, PT_HC)) return cudaErrorUnknown;
   if (!row_map(&maps.pages, a.pages, (uint64_t)a.n_pages * a.page, box ? box : 8)) return cudaErrorUnknown;
+  if (!row_map(&maps.rows, a.pages, (uint64_t)a.n_pages * a.page, 1)) return cudaErrorUnknown;
   if (a.W > 0) {
     if (!row_map(&maps.win, a.win, (uint64_t)a.B * a.W, PT_ROWS)) return cudaErrorUnknown;
   } else {
