@@ -4,11 +4,10 @@
 // Mathematics as in attention_paged.cu (an online softmax over 64-row tiles).  A CTA takes
 // 64 heads (the MMA M) and one unit of the schedule (paged.cuh): a run of tiles that may span
 // several sequences ("segments").  Per tile:
-//   1. a loader group brings the 64 rows into its stage of a two-stage ring, in 128-byte
-//      swizzle atoms: runs of pages as TMA boxes of gcd(page, 64) rows, scattered rows (selected
-//      entries, pages that share no factor of 8 with 64) by tile::gather4, tiles with absent rows
-//      by 16-byte cp.async with those rows zeroed (P = 0 there, and 0 * NaN must not reach the
-//      sums);
+//   1. the loader brings the 64 rows into a two-stage ring, in 128-byte swizzle atoms: runs of
+//      pages as TMA boxes of gcd(page, 64) rows, others (selected entries, pages that share no
+//      factor of 8 with 64, the last rows of a sequence) by tile::gather4.  Rows that are not
+//      attended are never copied: P = 0 there, but 0 * NaN must not reach the sums;
 //   2. one warp issues S = Q K^T (N = 64, 36 steps of K = 16) into TMEM;
 //   3. eight softmax warps read S, agree on the running maximum and write P to shared memory
 //      as two bf16 parts, P_hi = bf16(P) and P_lo = bf16(P - P_hi) (the second into the
@@ -33,12 +32,12 @@ constexpr int PT_ROWS = 64;              // rows per tile (N of QK^T, K of PV)
 constexpr int PT_HC = 64;                // heads per CTA (MMA M)
 constexpr int PT_ATOMS = 9;              // 576 dims = 9 atoms of 64 dims (128 bytes)
 constexpr int PT_LO = 4;                 // atoms of a tile's first half (dims 0-255)
-constexpr int PT_GROUP = 96;             // threads per loader group; group g fills stage g
+constexpr int PT_LDT = 192;              // loader threads
 constexpr int PT_SMW = 8;                // softmax warps: two warpgroups, one per half of a lane's columns
 constexpr int PT_SW = 8;                 // the warp of the queries and S
 constexpr int PT_PVW = 9;                // the warp of PV
 constexpr int PT_LDW = 10;               // first loader warp
-constexpr int PT_THREADS = PT_LDW * 32 + 2 * PT_GROUP;
+constexpr int PT_THREADS = PT_LDW * 32 + PT_LDT;
 constexpr int PT_MIN_TILES = 2;
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
@@ -51,15 +50,15 @@ struct PtSmem {
   uint8_t p[PT_HC * 128];                    // P_hi: 64 heads x 64 rows bf16; between segments the row sums
   float smax[2][2][128];                     // per tile parity and warpgroup: the lanes' tile maxima
   alignas(16) int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
-  uint32_t vmask[2][4][2];                   // per stage and use of it mod 4 (a group's warps may be a tile apart, the
-                                             // softmax another behind): bit j of word j / 32 set when row j is valid
+  uint32_t vmask[4][2];                      // per tile mod 4 (the loader's warps may be three tiles ahead of the
+                                             // softmax): bit j of word j / 32 set when row j exists
   uint64_t full[2][2], empty[2][2];          // per stage and half of the dims (0-255, 256-575)
   uint64_t sfull[2];
   uint64_t pfull, pdone, qfull, qfree, ofree, drain[2];
   uint64_t headb[2], segb;                   // softmax warps: the four of the same heads; all eight
   uint32_t tmem_base;
   int abort_flag;
-  int ld_stop[2];                            // per loader group: 1 + the step at which it stops (0 = running)
+  int ld_stop;                               // 1 + the tile at which the loader stops (0 = running)
 };
 static_assert(sizeof(PtSmem) <= 232448, "shared memory of one CTA (227 KB)");
 
@@ -67,15 +66,9 @@ struct PtMaps {
   CUtensorMap q;       // [B * H rows, 576], box 64 x 64
   CUtensorMap pages;   // [n_pages * page rows, 576], box 64 dims x box rows
   CUtensorMap win;     // [B * W rows, 576], box 64 x 64
-  CUtensorMap rows;    // the pages again, box 64 dims x 1 row (tile::gather4)
+  CUtensorMap rows, win_rows;   // pages and window again, box 64 dims x 1 row (tile::gather4)
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {   // bytes < 16: zero-filled
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-}
 __device__ __forceinline__ void named_bar(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -144,7 +137,6 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       }
       tc::mbar_init(&sm.sfull[s], 1);
       tc::mbar_init(&sm.drain[s], 1);
-      sm.ld_stop[s] = 0;
     }
     tc::mbar_init(&sm.pfull, PT_SMW);
     tc::mbar_init(&sm.pdone, 1);
@@ -154,6 +146,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     for (int s = 0; s < 2; ++s) tc::mbar_init(&sm.headb[s], 4);
     tc::mbar_init(&sm.segb, PT_SMW);
     sm.abort_flag = 0;
+    sm.ld_stop = 0;
     tc::fence_mbar_init();
   }
   if (warp == PT_SW) { tc::tmem_alloc(&sm.tmem_base, TM_COLS); tc::tmem_relinquish(); }
@@ -169,135 +162,129 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   tc::griddep_launch_dependents();                  // the merge waits for this grid itself
 
   if (warp >= PT_LDW) {
-    // ------------------------------------------------------------------ loader group g (96 threads)
-    const int g = (warp - PT_LDW) / (PT_GROUP / 32);
-    const int lg = threadIdx.x - PT_LDW * 32 - g * PT_GROUP;
-    // The group's next tile, resolved into registers before its stage is free: every other
-    // tile of the unit, counted over all segments.
+    // ------------------------------------------------------------------ loader (6 warps)
+    // Tile i of the unit, counted over all segments, goes to stage i % 2.  Thread j < 64 looks up row
+    // j of the tiles ahead, a step of the chain entry -> page -> row per tile, so that no load is
+    // waited for where it is issued.
+    const int lg = threadIdx.x - PT_LDW * 32;
+    struct Row {
+      bool is, in_a;                                  // a tile of the unit; of the entries (else of the window)
+      int b, e, id;                                   // sequence; entry (or the window's row), -1 = none; page id
+    };
     int64_t t = 0;
-    bool more = seg.next(a), in_a = true;
+    bool more = seg.next(a);
     if (more) t = seg.t0;
-    int y = -1;
-    auto step = [&](int n) {                          // n tiles on
-      while (more && n > 0) {
-        if (t + n < seg.t1) { t += n; n = 0; }
-        else {
-          n -= (int)(seg.t1 - t);
-          more = seg.next(a);
-          if (more) t = seg.t0;
-        }
-      }
-    };
-    auto resolve = [&]() {
-      in_a = t < seg.ta;
-      y = -1;
+    auto entry_of = [&]() {                           // the next tile: the entry
+      Row r{more, t < seg.ta, seg.b, -1, 0};
+      if (!more) return r;
       if (lg < PT_ROWS) {
-        const int64_t v = (in_a ? t : t - seg.ta) * PT_ROWS + lg;
-        if (in_a) {
-          if (v < seg.na) y = (int)paged_row(a, seg.b, (int)v);
-        } else if (v < seg.nw) {
-          y = seg.b * a.W + (int)v;
-        }
+        const int64_t v = (r.in_a ? t : t - seg.ta) * PT_ROWS + lg;
+        if (!r.in_a) r.e = v < seg.nw ? seg.b * a.W + (int)v : -1;
+        else if (v < seg.na) r.e = SPARSE ? a.idx[(size_t)seg.b * a.k + v] : (int)v;
       }
+      if (++t == seg.t1) {
+        more = seg.next(a);
+        t = seg.t0;
+      }
+      return r;
     };
-    step(g);
-    if (more) resolve();
-    int n_lo = 0, n_hi = 0;                           // halves this group started (for the drain)
-    for (int i = 0; more; ++i) {
+    auto page_of = [&](Row r) {                       // its page
+      if (r.in_a && r.e >= 0 && (!SPARSE || r.e < paged_capacity(a)))
+        r.id = a.table[(size_t)r.b * a.table_w + (unsigned)r.e / (unsigned)a.page];
+      else r.id = -1;
+      return r;
+    };
+    auto row_of = [&](const Row& r) {                 // its row of the pool or the window, -1 = none
+      if (!r.in_a || r.e < 0) return r.e;
+      if (r.id < 0 || r.id >= a.n_pages) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
+      return (int)((int64_t)r.id * a.page + (unsigned)r.e % (unsigned)a.page);
+    };
+    Row now = entry_of(), next = entry_of(), after = entry_of();
+    now = page_of(now);
+    next = page_of(next);
+    int n_full[2][2] = {{0, 0}, {0, 0}};              // per stage and half: copies started (for the drain)
+    for (int i = 0; now.is; ++i) {
+      const int st = i & 1, y = row_of(now);
+      const bool in_a = now.in_a;
+      const uint32_t ph = ((i >> 1) & 1) ^ 1;
       // what needs no free stage comes first: the rows, which of them exist, how they are copied
-      if (*(volatile int*)&sm.abort_flag) sm.ld_stop[g] = i + 1;      // the group leaves together below
+      if (*(volatile int*)&sm.abort_flag) sm.ld_stop = i + 1;         // the warps leave together below
       if (lg < PT_ROWS) {
-        sm.rowy[g][lg] = y;                           // (the group's copies of the tile before are issued)
+        sm.rowy[st][lg] = y;                          // (every warp is past the copies of two tiles before)
         const uint32_t vb = __ballot_sync(0xffffffffu, y >= 0);
-        if ((lg & 31) == 0) sm.vmask[g][i & 3][lg >> 5] = vb;
+        if ((lg & 31) == 0) sm.vmask[i & 3][lg >> 5] = vb;
       }
-      const bool a_tile = in_a;
-      named_bar(1 + g, PT_GROUP);
-      const int stop = *(volatile int*)&sm.ld_stop[g];
+      named_bar(1, PT_LDT);
+      const int stop = *(volatile int*)&sm.ld_stop;
       if (stop != 0 && stop <= i + 1) break;
-      const bool all = (sm.vmask[g][i & 3][0] & sm.vmask[g][i & 3][1]) == 0xffffffffu;
-      const int rows = a_tile ? box : PT_ROWS;        // rows per TMA box; box 0: pages that no box fits
-      const bool tma = all && (a_tile ? !SPARSE && box > 0 : true);
-      const uint32_t ph = (i & 1) ^ 1;
+      const uint32_t v0 = sm.vmask[i & 3][0], v1 = sm.vmask[i & 3][1];
+      const int rows = in_a ? box : PT_ROWS;          // rows per TMA box; box 0: pages that no box fits
       bool in_time = true;
-      // dims 0-255 as soon as the PV of the stage's last tile is past them, then the rest
-      if (tma) {
-        // the first thread of each box
+      // each way: dims 0-255 as soon as the PV of the stage's last tile is past them, then the rest
+      if ((v0 & v1) == 0xffffffffu && (in_a ? !SPARSE && box > 0 : true)) {
+        // a run of rows, or of pages: the first thread of each box
         if (lg < PT_ROWS && lg % rows == 0) {
-          const CUtensorMap* m = a_tile ? &maps.pages : &maps.win;
-#pragma unroll
+          const CUtensorMap* m = in_a ? &maps.pages : &maps.win;
+#pragma unroll 1
           for (int x = 0; x < 2; ++x) {
             const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
-            in_time = in_time && tc::mbar_wait(&sm.empty[g][x], ph);
+            in_time = in_time && tc::mbar_wait(&sm.empty[st][x], ph);
             if (!in_time) break;
-            if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[g][x], (at1 - at0) * ATOM);
+            if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[st][x], (at1 - at0) * ATOM);
             for (int at = at0; at < at1; ++at)
-              tc::tma_load_2d(sm.kv[g][at] + lg * 128, m, &sm.full[g][x], 64 * at, y);
-            if (x) ++n_hi; else ++n_lo;
+              tc::tma_load_2d(sm.kv[st][at] + lg * 128, m, &sm.full[st][x], 64 * at, y);
+            ++n_full[st][x];
           }
         }
         __syncwarp();
-      } else if (all) {
-        // 64 scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp
-        // starts 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the
-        // issue slots and shared-memory ports that the softmax uses).
+      } else if ((v0 | v1) != 0u) {
+        // scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp starts
+        // 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the issue slots
+        // and shared-memory ports that the softmax uses).  An absent row is a second copy of one
+        // that is there: its P is 0, and what it holds must not be less finite than the rest.
+        const int there = sm.rowy[st][v0 ? __ffs(v0) - 1 : 31 + __ffs(v1)];
+        const CUtensorMap* m = in_a ? &maps.rows : &maps.win_rows;
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
           const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
-          in_time = tc::mbar_wait(&sm.empty[g][x], ph) && in_time;
+          in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || tc::mbar_wait(&sm.empty[st][x], ph)));
           if (!in_time) break;
-          if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[g][x], (at1 - at0) * ATOM);
-          for (int p = (lg & 31) * (PT_GROUP / 32) + (lg >> 5); p < (at1 - at0) * (PT_ROWS / 4); p += PT_GROUP) {
+          if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[st][x], (at1 - at0) * ATOM);
+          for (int p = lane * (PT_LDT / 32) + (lg >> 5); p < (at1 - at0) * (PT_ROWS / 4); p += PT_LDT) {
             const int quad = p & (PT_ROWS / 4 - 1), at = at0 + p / (PT_ROWS / 4);
-            const int4 r = *reinterpret_cast<const int4*>(&sm.rowy[g][4 * quad]);
-            tc::tma_gather4(sm.kv[g][at] + quad * 512, &maps.rows, &sm.full[g][x], 64 * at, r);
+            int4 r = *reinterpret_cast<const int4*>(&sm.rowy[st][4 * quad]);
+            r.x = r.x < 0 ? there : r.x;
+            r.y = r.y < 0 ? there : r.y;
+            r.z = r.z < 0 ? there : r.z;
+            r.w = r.w < 0 ? there : r.w;
+            tc::tma_gather4(sm.kv[st][at] + quad * 512, m, &sm.full[st][x], 64 * at, r);
           }
-          if (x) ++n_hi; else ++n_lo;
+          ++n_full[st][x];
         }
-        __syncwarp();
-        named_bar(1 + g, PT_GROUP);                   // the rows are read
       } else {
-        const uint8_t* base = reinterpret_cast<const uint8_t*>(a_tile ? a.pages : a.win);
-        const uint32_t kv0 = tc::smem_u32(sm.kv[g][0]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
-          in_time = tc::mbar_wait(&sm.empty[g][x], ph) && in_time;
-          const int n = (at1 - at0) * 8;              // 16-byte chunks of a row's half
-          int j = lg / n, c = lg - j * n;
-          const int dj = PT_GROUP / n, dc = PT_GROUP - dj * n;
-          while (j < PT_ROWS) {
-            const int yr = sm.rowy[g][j], ch = at0 * 8 + c;
-            cp_async16(kv0 + (ch >> 3) * ATOM + sw128_off(j, ch & 7), base + (size_t)(yr < 0 ? 0 : yr) * (576 * 2) + ch * 16,
-                       yr < 0 ? 0 : 16);
-            c += dc;
-            j += dj;
-            if (c >= n) { c -= n; j += 1; }
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
+        // no row at all: zeros
+        in_time = __all_sync(0xffffffffu, lane != 0 || (tc::mbar_wait(&sm.empty[st][0], ph) && tc::mbar_wait(&sm.empty[st][1], ph)));
+        uint4* z = reinterpret_cast<uint4*>(sm.kv[st][0]);
+        for (int p = lg; p < PT_ATOMS * ATOM / 16 && in_time; p += PT_LDT) z[p] = make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_proxy_async_smem();
+        named_bar(1, PT_LDT);
+        if (lg == 0) {
+          tc::mbar_arrive(&sm.full[st][0]);
+          tc::mbar_arrive(&sm.full[st][1]);
         }
-        ++n_lo;
-        ++n_hi;
+        ++n_full[st][0];
+        ++n_full[st][1];
       }
       if (!in_time) atomicExch(&sm.abort_flag, 1);
-      if (!tma && !all) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        tc::fence_proxy_async_smem();
-        named_bar(1 + g, PT_GROUP);
-        if (lg == 0) tc::mbar_arrive(&sm.full[g][0]);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        tc::fence_proxy_async_smem();
-        named_bar(1 + g, PT_GROUP);
-        if (lg == 0) tc::mbar_arrive(&sm.full[g][1]);
-      }
-      // the next tile's rows, looked up while this one is worked on
-      step(2);
-      if (more) resolve();
+      now = next;
+      next = page_of(after);
+      after = entry_of();
     }
-    cp_async_wait_all();
     // drain: no TMA write of this CTA may be in flight when the CTA exits
-    if (lg == 0 && n_lo > 0) tc::mbar_wait(&sm.full[g][0], (n_lo - 1) & 1);
-    if (lg == 0 && n_hi > 0) tc::mbar_wait(&sm.full[g][1], (n_hi - 1) & 1);
+    if (lg == 0)
+      for (int q = 0; q < 4; ++q)
+        if (n_full[q >> 1][q & 1] > 0) tc::mbar_wait(&sm.full[q >> 1][q & 1], (n_full[q >> 1][q & 1] - 1) & 1);
+    __syncwarp();
   } else if (warp == PT_SW) {
     // ------------------------------------------------------------------ queries and S = Q K^T
     // The whole warp runs the loop (descriptors stay warp-uniform), one elected lane issues.  S
@@ -443,7 +430,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         const int st = i & 1;
         const uint32_t ph = (i >> 1) & 1;
         bool w = tc::mbar_wait(&sm.full[st][0], ph);  // the mask of the tile's rows
-        const uint32_t vm = sm.vmask[st][(i >> 1) & 3][half] >> (16 * wg);
+        const uint32_t vm = sm.vmask[i & 3][half] >> (16 * wg);
         w = w && tc::mbar_wait(&sm.sfull[st], ph);
         w = __all_sync(0xffffffffu, w && !*(volatile int*)&sm.abort_flag);
         if (!w) { ok = false; break; }
@@ -675,8 +662,9 @@ cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
   if (!row_map(&maps.rows, a.pages, (uint64_t)a.n_pages * a.page, 1)) return cudaErrorUnknown;
   if (a.W > 0) {
     if (!row_map(&maps.win, a.win, (uint64_t)a.B * a.W, PT_ROWS)) return cudaErrorUnknown;
+    if (!row_map(&maps.win_rows, a.win, (uint64_t)a.B * a.W, 1)) return cudaErrorUnknown;
   } else {
-    maps.win = maps.pages;                           // no tile is ever a window tile
+    maps.win = maps.win_rows = maps.rows;            // no tile is ever a window tile
   }
   auto kern = a.idx ? paged_attn_tc_kernel<true> : paged_attn_tc_kernel<false>;
   static std::atomic<uint64_t> ready[2];               // bit per device: the kernel's shared-memory size is set
