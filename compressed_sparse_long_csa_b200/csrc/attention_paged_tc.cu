@@ -159,7 +159,6 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   const uint32_t tmem = sm.tmem_base;
   SegIter seg;
   seg.start(plan, unit);
-  tc::griddep_launch_dependents();                  // the merge waits for this grid itself
 
   if (warp >= PT_LDW) {
     // ------------------------------------------------------------------ loader (6 warps)
@@ -607,6 +606,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   }
   tc::fence_before_sync();
   __syncthreads();
+  tc::griddep_launch_dependents();                  // the merge (which waits for this grid) may take the SM
   if (sm.abort_flag && threadIdx.x == 0) raise_err(a.err, CSA_DEVERR_TIMEOUT);
   if (warp == PT_SW) {
     tc::fence_after_sync();
