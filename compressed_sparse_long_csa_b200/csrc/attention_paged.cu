@@ -71,17 +71,12 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
     if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
   }
   if (hg == 0 && threadIdx.x == 0) paged_note(a, plan, unit);
-  int64_t left = min(plan.per, plan.total - (int64_t)unit * plan.per);
-  int b = plan.b;
-  int64_t t = (int64_t)unit * plan.per - plan.before;
-  for (; left > 0; ++b, t = 0) {
-    const int na = paged_rows_a(a, b), nw = paged_rows_w(a, b);
-    const int64_t ta = ((int64_t)na + PC_ROWS - 1) / PC_ROWS, tiles = ta + (nw + PC_ROWS - 1) / PC_ROWS;
-    if (t >= tiles) continue;
-    const int64_t t1 = min(tiles, t + left);
-    const bool whole = t == 0 && t1 == tiles;
-    const int slot = 2 * unit + (t == 0 ? 1 : 0);
-    left -= t1 - t;
+  PagedSeg seg;
+  seg.start(plan, unit);
+  while (seg.next(a)) {
+    const int b = seg.b, na = seg.na, nw = seg.nw;
+    const int64_t ta = seg.ta, t1 = seg.t1;
+    int64_t t = seg.t0;
     // the lane's row of a tile: in the pool or the window, -1 = none
     auto resolve = [&](int64_t tile) {
       if (tile >= t1) return -1;
@@ -172,7 +167,7 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
       else if (t + 1 < t1) copy(t + 1, row, 0);
     }
     if (!hv) continue;
-    if (whole) {
+    if (seg.whole) {
       const float sk = a.sink[h], M = fmaxf(sk, m_run);
       float den = 0.f, f = 0.f;
       if (M != -INFINITY) {
@@ -193,7 +188,7 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
       }
       if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = den > 0.f ? M + logf(den) : -INFINITY;
     } else {
-      float* blk = a.part + (size_t)slot * paged_part_block(a.H, dv);
+      float* blk = a.part + (size_t)seg.slot(unit) * paged_part_block(a.H, dv);
 #pragma unroll
       for (int i = 0; i < NO; ++i) {
         const int c = 4 * lane + 128 * i;
@@ -216,9 +211,35 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
 // over, they share its pieces.  All sums run in a fixed order, so a result does not depend
 // on the order in which the units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece, and
 // the latency of its few round trips.
-constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 8, PM_PER_SM = 3;
+constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 8, PM_PER_SM = 2;
+constexpr int PM_FEW = 8;        // partials that one warp joins by itself
 // Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)
 constexpr size_t pm_unit_bytes(bool part16) { return PM_H * (sizeof(float4) + (part16 ? sizeof(float2) : 0)) + sizeof(int4); }
+// acc += w times a 16-byte piece of a partial
+template <bool PART16>
+__device__ __forceinline__ void merge_add(float* acc, const uint4& v, float w) {
+  const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (PART16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u4[q]));
+      acc[2 * q] = fmaf(w, f.x, acc[2 * q]);
+      acc[2 * q + 1] = fmaf(w, f.y, acc[2 * q + 1]);
+    } else {
+      acc[q] = fmaf(w, __uint_as_float(u4[q]), acc[q]);
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void merge_store(T* dst, const float* v) {
+  if constexpr (V == Elem<T>::VEC) {
+    Elem<T>::st_vec(dst, v);
+  } else {
+#pragma unroll
+    for (int u = 0; u < V; ++u) Elem<T>::st(dst + u, v[u]);
+  }
+}
+
 template <typename T, bool PART16>
 __global__ void __launch_bounds__(PM_THREADS, PM_PER_SM)
 paged_merge_kernel(PagedAttnArgs a) {
@@ -230,35 +251,113 @@ paged_merge_kernel(PagedAttnArgs a) {
   float2* const s23 = reinterpret_cast<float2*>(wts + (size_t)a.units * PM_H);
   __shared__ float red[2][PM_THREADS / 32][PM_H];
   __shared__ float sums[V][PM_THREADS];
-  __shared__ int count;
+  __shared__ int counts[2];
   const int dv = a.dv, H = a.H;
   const int hl = threadIdx.x & (PM_H - 1), j = threadIdx.x / PM_H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the list: sequences of few partials from the front, the others from the back
   if (warp == 0) {
     const int2* notes = paged_notes(a);
-    int n = 0;
+    int few = 0, many = 0;
 #pragma unroll 4
     for (int u0 = 0; u0 < a.units; u0 += 32) {
       const int2 note = u0 + lane < a.units ? __ldcg(&notes[u0 + lane]) : make_int2(-1, 0);
-      const unsigned m = __ballot_sync(0xffffffffu, note.y > 0);
-      if (note.y > 0) list[n + __popc(m & ((1u << lane) - 1u))] = make_int4(u0 + lane, note.x, note.y, 0);
-      n += __popc(m);
+      const unsigned f = __ballot_sync(0xffffffffu, note.y > 0 && note.y <= PM_FEW), m = __ballot_sync(0xffffffffu, note.y > PM_FEW);
+      const unsigned below = (1u << lane) - 1u;
+      if (note.y > 0)
+        list[note.y <= PM_FEW ? few + __popc(f & below) : a.units - 1 - many - __popc(m & below)] =
+            make_int4(u0 + lane, note.x, note.y, 0);
+      few += __popc(f);
+      many += __popc(m);
     }
-    if (lane == 0) count = n;
+    if (lane == 0) { counts[0] = few; counts[1] = many; }
   }
   __syncthreads();
+  const int count = counts[1];
   const int hb = (H + PM_H - 1) / PM_H, pieces = dv / V;
   int slices = 1;
   while (slices < PM_SLICES && 2 * count * hb * slices <= (int)gridDim.x && pieces / slices > 4) slices <<= 1;
   const int width = (pieces + slices - 1) / slices;   // 16-byte pieces of a slice
+  const size_t block = paged_part_block(H, dv);
+  {
+    // Few partials: a warp takes eight heads and 8 pieces of the dims.  Lane (head, q): partials q and
+    // q + 4 in the weights, pieces q and q + 4 in the sums; all loads are one round trip.
+    const int q = lane >> 3, wide = (pieces + 7) / 8;
+    for (int item = blockIdx.x * (PM_THREADS / 32) + warp; item < counts[0] * hb * wide; item += gridDim.x * (PM_THREADS / 32)) {
+      const int cg = item % wide, blk8 = item / wide % hb;
+      const int4 cut = list[item / (wide * hb)];
+      const int b = cut.y, n = cut.z, h = blk8 * PM_H + hl;
+      const bool hv = h < H;
+      const int hc = hv ? h : H - 1;
+      const float* part = a.part + (size_t)(2 * cut.x) * block;
+      auto partial = [&](int p) { return part + (p ? 2 * p * block : block); };
+      uint4 x[2][PM_FEW];
+#pragma unroll
+      for (int u = 0; u < PM_FEW; ++u) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = cg * 8 + 4 * k + q;
+          if (u < n && c < pieces) x[k][u] = __ldcg(reinterpret_cast<const uint4*>(partial(u)) + (size_t)c * H + hc);
+        }
+      }
+      const size_t rec = paged_part_rec(H, dv, hc);
+      const float sk = a.sink[hc];
+      float m[2], l[2], w[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int p = q + 4 * k;
+        m[k] = -INFINITY;
+        l[k] = 0.f;
+        w[k] = 1.f;
+        if (p < n) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(partial(p) + rec));
+          if (PART16) w[k] = __ldcg(partial(p) + rec + 2 + ((cg * 8) >> 4));      // 16 pieces a quarter
+          m[k] = ml.x;
+          l[k] = ml.y;
+        }
+      }
+      float M = fmaxf(m[0], m[1]);
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+      M = fmaxf(fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16)), sk);
+      float den = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float e = m[k] == -INFINITY ? 0.f : __expf(m[k] - M);
+        den += e * l[k];
+        w[k] *= e;
+      }
+      den += __shfl_xor_sync(0xffffffffu, den, 8);
+      den += __shfl_xor_sync(0xffffffffu, den, 16);
+      den += sk == -INFINITY ? 0.f : __expf(sk - M);
+      const float inv = den > 0.f ? 1.f / den : 0.f;
+      float acc[2][V];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int u = 0; u < V; ++u) acc[k][u] = 0.f;
+#pragma unroll
+      for (int u = 0; u < PM_FEW; ++u) {
+        if (u < n) {
+          const float wu = __shfl_sync(0xffffffffu, w[u >> 2], hl + 8 * (u & 3)) * inv;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) merge_add<PART16>(acc[k], x[k][u], wu);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = cg * 8 + 4 * k + q;
+        if (hv && c < pieces) merge_store<T, V>((T*)a.out + ((size_t)b * H + h) * dv + V * c, acc[k]);
+      }
+      if (a.lse && cg == 0 && q == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+    }
+  }
   int gw = PM_C;                                      // threads along a slice; the other PM_C / gw share its partials
   while (gw > 4 && gw / 2 >= width) gw >>= 1;
   const int groups = PM_C / gw, g = j / gw, jc = j - g * gw;
-  const size_t block = paged_part_block(H, dv);
   for (int item = blockIdx.x; item < count * hb * slices; item += gridDim.x) {
     const int sl = item % slices, blk8 = item / slices % hb;
-    const int4 cut = list[item / (slices * hb)];
+    const int4 cut = list[a.units - 1 - item / (slices * hb)];
     const int b = cut.y, n = cut.z, h = blk8 * PM_H + hl;
     const bool hv = h < H;
     const int hc = hv ? h : H - 1;
@@ -269,30 +368,6 @@ paged_merge_kernel(PagedAttnArgs a) {
     const size_t rec = paged_part_rec(H, dv, hc);
     const float sk = a.sink[hc];
     float acc[V];
-    auto add = [&](const uint4& v, float w) {
-      const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (PART16) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u4[q]));
-          acc[2 * q % V] = fmaf(w, f.x, acc[2 * q % V]);
-          acc[(2 * q + 1) % V] = fmaf(w, f.y, acc[(2 * q + 1) % V]);
-        } else {
-          acc[q] = fmaf(w, __uint_as_float(u4[q]), acc[q]);
-        }
-      }
-    };
-    auto store = [&](int c, float inv) {
-      T* dst = (T*)a.out + ((size_t)b * H + h) * dv + V * c;
-#pragma unroll
-      for (int u = 0; u < V; ++u) acc[u] *= inv;
-      if constexpr (V == Elem<T>::VEC) {
-        Elem<T>::st_vec(dst, acc);
-      } else {
-#pragma unroll
-        for (int u = 0; u < V; ++u) Elem<T>::st(dst + u, acc[u]);
-      }
-    };
     const int cend = min(pieces, (sl + 1) * width);
     const int c0 = sl * width + jc;
     float M = sk;
@@ -346,9 +421,9 @@ paged_merge_kernel(PagedAttnArgs a) {
         }
 #pragma unroll
         for (int u = 0; u < PM_EARLY; ++u)
-          if (g + u * groups < n) add(x[u], wq[(g + u * groups) * PM_H * 4]);
+          if (g + u * groups < n) merge_add<PART16>(acc, x[u], wq[(g + u * groups) * PM_H * 4]);
 #pragma unroll 8
-        for (int p = g + PM_EARLY * groups; p < n; p += groups) add(load(p, c), wq[p * PM_H * 4]);
+        for (int p = g + PM_EARLY * groups; p < n; p += groups) merge_add<PART16>(acc, load(p, c), wq[p * PM_H * 4]);
       }
       if (groups > 1) {                               // (the slice is one round of its threads)
 #pragma unroll
@@ -358,7 +433,11 @@ paged_merge_kernel(PagedAttnArgs a) {
 #pragma unroll
           for (int u = 0; u < V; ++u) acc[u] += sums[u][threadIdx.x + o * gw * PM_H];
       }
-      if (g == 0 && c < cend && hv) store(c, inv);
+      if (g == 0 && c < cend && hv) {
+#pragma unroll
+        for (int u = 0; u < V; ++u) acc[u] *= inv;
+        merge_store<T, V>((T*)a.out + ((size_t)b * H + h) * dv + V * c, acc);
+      }
     }
     if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
     __syncthreads();                                  // the weights and sums are read
@@ -397,6 +476,7 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
   a.tile_log2 = 5;
   static_assert(PC_ROWS == 1 << 5, "tile rows");
   a.min_tiles = PC_MIN_TILES;
+  a.begin_cost = 0;
   a.units = paged_units(a, paged_units_cc(a.B, a.H, paged_rows_max(a)));
   const int warps = a.H < PC_WARPS ? a.H : PC_WARPS;
   auto go = [&](auto tag) {

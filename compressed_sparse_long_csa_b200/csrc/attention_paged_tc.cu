@@ -39,6 +39,7 @@ constexpr int PT_PVW = 9;                // the warp of PV
 constexpr int PT_LDW = 10;               // first loader warp
 constexpr int PT_THREADS = PT_LDW * 32 + PT_LDT;
 constexpr int PT_MIN_TILES = 2;
+constexpr int PT_BEGIN_COST = 2;
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;    // TMEM columns: O 256, S 2 x 32
@@ -88,39 +89,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // byte offset of 16-byte chunk c of row j in a 128-byte-swizzled atom
 __device__ __forceinline__ uint32_t sw128_off(int j, int c) { return (j >> 3) * 1024 + (j & 7) * 128 + ((c ^ (j & 7)) << 4); }
 
-// The segments of a unit: tiles [t0, t1) of sequence b.  Every role walks them by itself.
-struct SegIter {
-  int next_b;
-  int64_t next_t, left;
-  int b, na, nw;
-  int64_t ta, t0, t1;                        // ta: tiles of the entries; the window's follow
-  bool whole;
-  __device__ __forceinline__ void start(const PagedPlan& p, int unit) {
-    next_b = p.b;
-    next_t = (int64_t)unit * p.per - p.before;
-    left = p.total - (int64_t)unit * p.per;
-    if (left > p.per) left = p.per;
-    t0 = t1 = 0;
-  }
-  __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
-    while (left > 0) {
-      b = next_b++;
-      na = paged_rows_a(a, b);
-      nw = paged_rows_w(a, b);
-      ta = ((int64_t)na + PT_ROWS - 1) / PT_ROWS;
-      const int64_t tiles = ta + (nw + PT_ROWS - 1) / PT_ROWS;
-      t0 = next_t;
-      next_t = 0;
-      if (t0 >= tiles) continue;
-      t1 = tiles < t0 + left ? tiles : t0 + left;
-      left -= t1 - t0;
-      whole = t0 == 0 && t1 == tiles;
-      return true;
-    }
-    return false;
-  }
-};
-
 template <bool SPARSE>
 __global__ void __launch_bounds__(PT_THREADS, 1)
 paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant__ PagedAttnArgs a, int halves, int box) {
@@ -157,7 +125,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   tc::fence_proxy_async_smem();
   __syncthreads();                                  // the plan's scratch is read; Q may land there
   const uint32_t tmem = sm.tmem_base;
-  SegIter seg;
+  PagedSeg seg;                                     // every role walks the unit's segments by itself
   seg.start(plan, unit);
 
   if (warp >= PT_LDW) {
@@ -538,7 +506,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (!meet()) { ok = false; break; }             // P may be written again
       const float m = m_run * 0.6931471805599453f;
       float f = 1.f, M = 0.f, den = 0.f;
-      float* blk = a.part + (size_t)(2 * unit + (seg.t0 == 0 ? 1 : 0)) * paged_part_block(a.H, 512);
+      float* blk = a.part + (size_t)seg.slot(unit) * paged_part_block(a.H, 512);
       if (seg.whole) {
         M = fmaxf(sink, m);
         float e = 0.f;
@@ -651,6 +619,7 @@ cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
   a.tile_log2 = 6;
   static_assert(PT_ROWS == 1 << 6, "tile rows");
   a.min_tiles = PT_MIN_TILES;
+  a.begin_cost = PT_BEGIN_COST;
   a.units = paged_units(a, paged_units_tc(a.B, a.H, paged_rows_max(a)));
   // the largest of 64, 32, 16, 8 rows that divides the pages: every box lies in one page
   int box = PT_ROWS;

@@ -44,6 +44,7 @@ struct PagedAttnArgs {
   int units;                  // work units (CTAs per head group)
   int tile_log2;              // rows per tile of the schedule, as a power of two
   int min_tiles;              // least tiles of a unit
+  int begin_cost;             // what beginning a sequence costs a unit, in tiles
   unsigned* err;
 };
 
@@ -51,14 +52,15 @@ struct PagedAttnArgs {
 __host__ __device__ inline int64_t paged_capacity(const PagedAttnArgs& a) { return (int64_t)a.table_w * a.page; }
 
 // ---- schedule ---------------------------------------------------------------------------------
-// The rows of a sequence are cut into tiles of `tile` rows: its entries (or index slots)
-// first, then its window rows, so that no tile mixes the two.  The tiles of all sequences,
-// in order, are dealt to the units in equal runs of q tiles: every unit streams the same
-// number of rows however ragged the lengths are, and the lengths are read on the device
-// only.  A sequence whose tiles lie in one unit is finished there; one that is cut leaves a
-// partial (o, m, l) in each unit it touches, and a merge kernel joins them.  A unit holds at
-// most two pieces of cut sequences: one of a sequence that began before it (slot 0) and one
-// of a sequence that goes on after it (slot 1).
+// The rows of a sequence are cut into tiles of 2^tile_log2 rows: its entries (or index slots)
+// first, then its window rows, so that no tile mixes the two.  The tiles of all sequences, in
+// order, are dealt to the units in equal runs, so that every unit takes as long as the others
+// however ragged the lengths are; the lengths are read on the device only.  Beginning a sequence
+// costs a unit more than its tiles (queries, an empty pipeline, an epilogue): begin_cost places
+// that hold no tile come before a sequence's first one.  A sequence whose tiles lie in one unit is
+// finished there; one that is cut leaves a partial (o, m, l) in each unit it touches, and a merge
+// kernel joins them.  A unit holds at most two partials: one of a sequence that began before it
+// (slot 0) and one of a sequence that begins in it and goes on (slot 1).
 __device__ __forceinline__ int paged_rows_a(const PagedAttnArgs& a, int b) {
   if (a.idx) return a.k;
   const int64_t n = a.n_entries[b], cap = paged_capacity(a);
@@ -73,22 +75,27 @@ __device__ __forceinline__ int64_t paged_tiles(const PagedAttnArgs& a, int b) {
   const int na = paged_rows_a(a, b), nw = paged_rows_w(a, b), up = (1 << a.tile_log2) - 1;
   return (((int64_t)na + up) >> a.tile_log2) + ((nw + up) >> a.tile_log2);
 }
+// Places of a sequence: its tiles and what it costs to begin it.
+__device__ __forceinline__ int64_t paged_places(const PagedAttnArgs& a, int b) {
+  const int64_t tiles = paged_tiles(a, b);
+  return tiles ? tiles + a.begin_cost : 0;
+}
 
 struct PagedPlan {
-  int64_t total;     // tiles of all sequences
-  int64_t per;       // tiles of a unit
-  int64_t before;    // tiles of the sequences before sequence b
-  int b;             // the sequence that holds the unit's first tile (B when there is none)
+  int64_t total;     // places of all sequences
+  int64_t per;       // places of a unit
+  int64_t before;    // places of the sequences before sequence b
+  int b;             // the sequence that holds the unit's first place (B when there is none)
 };
 
-// The plan, and the sequence that holds tile unit * per.  All `threads` threads of the block
-// call it; scratch: 66 int64 in shared memory.
+// The plan of a unit.  All `threads` threads of the block call it; scratch: 66 int64 in shared
+// memory.
 __device__ __forceinline__ PagedPlan paged_plan(const PagedAttnArgs& a, int unit, int threads, int64_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
   const int chunk = (a.B + threads - 1) / threads;
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += paged_tiles(a, b);
+  for (int b = b0; b < b1; ++b) mine += paged_places(a, b);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -98,7 +105,7 @@ __device__ __forceinline__ PagedPlan paged_plan(const PagedAttnArgs& a, int unit
   if (lane == 31) scratch[warp] = incl;
   if (tid == 0) { scratch[64] = 0; scratch[65] = a.B; }
   __syncthreads();
-  int64_t at = incl - mine, total = 0;                // tiles before this thread's sequences, and all
+  int64_t at = incl - mine, total = 0;                // places before this thread's sequences, and all
   for (int w = 0; w < warps; ++w) {
     const int64_t v = scratch[w];
     if (w < warp) at += v;
@@ -110,7 +117,7 @@ __device__ __forceinline__ PagedPlan paged_plan(const PagedAttnArgs& a, int unit
   if (first >= at && first < at + mine) {             // one thread at most
     int b = b0;
     for (;; ++b) {
-      const int64_t n = paged_tiles(a, b);
+      const int64_t n = paged_places(a, b);
       if (first < at + n) break;
       at += n;
     }
@@ -125,6 +132,45 @@ __device__ __forceinline__ PagedPlan paged_plan(const PagedAttnArgs& a, int unit
   p.b = (int)scratch[65];
   return p;
 }
+
+// The segments of a unit: tiles [t0, t1) of sequence b.
+struct PagedSeg {
+  int next_b;
+  int64_t next_p, left;                      // the next place of next_b; places left of the unit
+  int b, na, nw;
+  int64_t ta, t0, t1;                        // ta: tiles of the entries; the window's follow
+  bool whole;                                // all tiles of the sequence
+  __device__ __forceinline__ void start(const PagedPlan& p, int unit) {
+    next_b = p.b;
+    next_p = (int64_t)unit * p.per - p.before;
+    left = p.total - (int64_t)unit * p.per;
+    if (left > p.per) left = p.per;
+    t0 = t1 = 0;
+  }
+  __device__ __forceinline__ bool next(const PagedAttnArgs& a) {
+    const int up = (1 << a.tile_log2) - 1;
+    while (left > 0) {
+      b = next_b++;
+      na = paged_rows_a(a, b);
+      nw = paged_rows_w(a, b);
+      ta = ((int64_t)na + up) >> a.tile_log2;
+      const int64_t tiles = ta + ((nw + up) >> a.tile_log2);
+      const int64_t p0 = next_p, end = tiles ? tiles + a.begin_cost : 0;
+      next_p = 0;
+      if (p0 >= end) continue;
+      const int64_t p1 = end < p0 + left ? end : p0 + left;
+      left -= p1 - p0;
+      t0 = p0 > a.begin_cost ? p0 - a.begin_cost : 0;
+      t1 = p1 > a.begin_cost ? p1 - a.begin_cost : 0;
+      if (t0 >= t1) continue;                // the unit holds the cost of the beginning only
+      whole = t0 == 0 && t1 == tiles;
+      return true;
+    }
+    return false;
+  }
+  // The slot of the segment's partial.
+  __device__ __forceinline__ int slot(int unit) const { return 2 * unit + (t0 == 0 ? 1 : 0); }
+};
 
 // A partial of a cut sequence holds o (not normalised), m and l per head, for natural-log
 // logits, in one of two forms:
@@ -147,15 +193,15 @@ __host__ __device__ inline int2* paged_notes(const PagedAttnArgs& a) {
 }
 // Writes the unit's note (one thread).
 __device__ __forceinline__ void paged_note(const PagedAttnArgs& a, const PagedPlan& p, int unit) {
-  const int64_t end = (int64_t)(unit + 1) * p.per;    // first tile of the next unit
+  const int64_t end = (int64_t)(unit + 1) * p.per;    // first place of the next unit
   int2 note = make_int2(-1, 0);
   if (end < p.total) {
     int64_t at = p.before;
-    int b = p.b;
-    for (;; ++b) {                                    // the sequence that holds tile end - 1
-      const int64_t n = paged_tiles(a, b);
-      if (end - 1 < at + n) {
-        if (end < at + n && at >= end - p.per) note = make_int2(b, (int)((at + n - 1) / p.per) - unit + 1);
+    for (int b = p.b;; ++b) {                         // the sequence that holds place `end`
+      const int64_t n = paged_places(a, b);
+      if (end < at + n) {
+        const int64_t first = at + a.begin_cost;      // of its first tile
+        if (first < end && first >= end - p.per) note = make_int2(b, (int)((at + n - 1) / p.per) - unit + 1);
         break;
       }
       at += n;
