@@ -371,12 +371,27 @@ paged_merge_kernel(PagedAttnArgs a) {
     const int cend = min(pieces, (sl + 1) * width);
     const int c0 = sl * width + jc;
     float M = sk;
-    for (int p = j; p < n; p += PM_C) {
-      const float4* r = reinterpret_cast<const float4*>(partial(p) + rec);
-      const float4 r0 = __ldcg(r);
-      if (PART16) s23[p * PM_H + hl] = __ldcg(reinterpret_cast<const float2*>(r + 1));
-      wts[p * PM_H + hl] = r0;
-      M = fmaxf(M, r0.x);
+    for (int p0 = j; p0 < n; p0 += 4 * PM_C) {        // four records' loads at a time
+      float4 r0[4];
+      float2 r1[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int p = p0 + u * PM_C;
+        if (p < n) {
+          const float4* r = reinterpret_cast<const float4*>(partial(p) + rec);
+          r0[u] = __ldcg(r);
+          if (PART16) r1[u] = __ldcg(reinterpret_cast<const float2*>(r + 1));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int p = p0 + u * PM_C;
+        if (p < n) {
+          wts[p * PM_H + hl] = r0[u];
+          if (PART16) s23[p * PM_H + hl] = r1[u];
+          M = fmaxf(M, r0[u].x);
+        }
+      }
     }
     // the group's first partials are on their way while the weights are formed
     uint4 x[PM_EARLY];
