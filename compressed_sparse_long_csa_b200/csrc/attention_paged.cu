@@ -64,11 +64,15 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // the merge waits for this grid itself
   const PagedPlan plan = paged_plan(a, unit, threads, scratch);
-  // sequences without a row: no unit has a tile of theirs
-  for (int b = unit; b < a.B; b += a.units) {
-    if (paged_tiles(a, b) != 0 || !hv) continue;
-    for (int c = lane; c < dv; c += 32) Elem<T>::st((T*)a.out + ((size_t)b * a.H + h) * dv + c, 0.f);
-    if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
+  // sequences without a row (no unit has a tile of theirs): a lane looks at each, the warp clears
+  for (int b0 = unit; b0 < a.B; b0 += 32 * a.units) {
+    const int64_t bl = (int64_t)b0 + (int64_t)lane * a.units;
+    for (unsigned none = __ballot_sync(0xffffffffu, bl < a.B && paged_tiles(a, (int)min(bl, (int64_t)a.B - 1)) == 0); none; none &= none - 1) {
+      const int b = b0 + (__ffs(none) - 1) * a.units;
+      if (!hv) continue;
+      for (int c = lane; c < dv; c += 32) Elem<T>::st((T*)a.out + ((size_t)b * a.H + h) * dv + c, 0.f);
+      if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
+    }
   }
   if (hg == 0 && threadIdx.x == 0) paged_note(a, plan, unit);
   PagedSeg seg;
@@ -211,7 +215,7 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
 // over, they share its pieces.  All sums run in a fixed order, so a result does not depend
 // on the order in which the units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece, and
 // the latency of its few round trips.
-constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 8, PM_PER_SM = 2;
+constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 5, PM_PER_SM = 2;
 constexpr int PM_FEW = 8;        // partials that one warp joins by itself
 // Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)
 constexpr size_t pm_unit_bytes(bool part16) { return PM_H * (sizeof(float4) + (part16 ? sizeof(float2) : 0)) + sizeof(int4); }
@@ -260,7 +264,7 @@ paged_merge_kernel(PagedAttnArgs a) {
   if (warp == 0) {
     const int2* notes = paged_notes(a);
     int few = 0, many = 0;
-#pragma unroll 4
+#pragma unroll 1
     for (int u0 = 0; u0 < a.units; u0 += 32) {
       const int2 note = u0 + lane < a.units ? __ldcg(&notes[u0 + lane]) : make_int2(-1, 0);
       const unsigned f = __ballot_sync(0xffffffffu, note.y > 0 && note.y <= PM_FEW), m = __ballot_sync(0xffffffffu, note.y > PM_FEW);
@@ -393,11 +397,6 @@ paged_merge_kernel(PagedAttnArgs a) {
         }
       }
     }
-    // the group's first partials are on their way while the weights are formed
-    uint4 x[PM_EARLY];
-#pragma unroll
-    for (int u = 0; u < PM_EARLY; ++u)
-      if (g + u * groups < n && c0 < cend) x[u] = load(g + u * groups, c0);
 #pragma unroll
     for (int o = PM_H; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane < PM_H) red[0][warp][lane] = M;
@@ -429,16 +428,16 @@ paged_merge_kernel(PagedAttnArgs a) {
       for (int u = 0; u < V; ++u) acc[u] = 0.f;
       const float* wq = reinterpret_cast<const float*>(wts + hl) + (PART16 ? (c >> 4) & 3 : 0);
       if (c < cend) {
-        if (c != c0) {
+#pragma unroll 1
+        for (int p0 = g; p0 < n; p0 += PM_EARLY * groups) {
+          uint4 x[PM_EARLY];
 #pragma unroll
           for (int u = 0; u < PM_EARLY; ++u)
-            if (g + u * groups < n) x[u] = load(g + u * groups, c);
-        }
+            if (p0 + u * groups < n) x[u] = load(p0 + u * groups, c);
 #pragma unroll
-        for (int u = 0; u < PM_EARLY; ++u)
-          if (g + u * groups < n) merge_add<PART16>(acc, x[u], wq[(g + u * groups) * PM_H * 4]);
-#pragma unroll 8
-        for (int p = g + PM_EARLY * groups; p < n; p += groups) merge_add<PART16>(acc, load(p, c), wq[p * PM_H * 4]);
+          for (int u = 0; u < PM_EARLY; ++u)
+            if (p0 + u * groups < n) merge_add<PART16>(acc, x[u], wq[(p0 + u * groups) * PM_H * 4]);
+        }
       }
       if (groups > 1) {                               // (the slice is one round of its threads)
 #pragma unroll
