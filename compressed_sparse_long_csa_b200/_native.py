@@ -384,6 +384,10 @@ def latent_append_paged(rows, entry, pages, block_table, seq=None, pos=None, inv
         if q_pe.shape != (T, H, d_r) or q_pe.dtype != dt or q_pe.get_device() != di or q_pe.stride(2) != 1:
             _unfit(name, "q_pe", q_pe, f"[{T}, {H}, {d_r}] {dt} with a dense last dimension")
         ld_t, ld_h, _ = q_pe.stride()
+        if T == 1:
+            ld_t = 0                       # the stride of a single row or head means nothing
+        if H == 1:
+            ld_h = 0
         qp, qo = q_pe.data_ptr(), q.data_ptr()
     elif q is not None or q_pe is not None:
         raise CsaError(f"{name}: q and q_pe come together")

@@ -380,15 +380,21 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       return __all_sync(0xffffffffu, tc::mbar_wait(&sm.segb, met++ & 1));
     };
     // logits in the base-2 domain: P = 2^(s - m)
-    const float scale2 = a.sm_scale * 1.4426950408889634f, scale = fabsf(scale2);
+    const float scale2 = a.sm_scale * 1.4426950408889634f;
+    const float scale = fmaxf(fabsf(scale2), 1.2e-38f);          // not 0: an absent row's -inf must stay one
     bool ok = true;
     int i = 0;                                        // tiles so far, over all segments
-    // sequences without a row (no unit has a tile of theirs)
-    for (int b = unit; b < a.B; b += a.units) {
-      if (paged_rows_a(a, b) != 0 || paged_rows_w(a, b) != 0 || !hv) continue;
-      uint4* o = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + ((size_t)b * a.H + h) * 512 + 256 * wg + 128 * half);
-      for (int c = 0; c < 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse && tl < 64 && wg == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
+    // sequences without a row (no unit has a tile of theirs): a lane looks at each, the warp clears
+    for (int b0 = unit + warp * 32 * a.units; b0 < a.B; b0 += PT_SMW * 32 * a.units) {
+      const int64_t bl = (int64_t)b0 + (int64_t)lane * a.units;
+      const bool none = bl < a.B && paged_rows_a(a, (int)bl) == 0 && paged_rows_w(a, (int)bl) == 0;
+      for (unsigned left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
+        const int b = b0 + (__ffs(left) - 1) * a.units, n = min(PT_HC, a.H - hh * PT_HC);
+        uint4* o = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + ((size_t)b * a.H + hh * PT_HC) * 512);
+        for (int c = lane; c < n * 64; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse)
+          for (int c = hh * PT_HC + lane; c < hh * PT_HC + n; c += 32) a.lse[(size_t)b * a.H + c] = a.sink[c];
+      }
     }
     __syncwarp();
     if (threadIdx.x == 0 && hh == 0) paged_note(a, plan, unit);
