@@ -19,9 +19,10 @@ namespace csa {
 namespace {
 
 constexpr int PC_ROWS = 32;      // rows per tile: one lane per row in the logits
-constexpr int PC_WARPS = 8;      // heads per CTA: one warp each
-constexpr int PC_MAXD = 576;
+constexpr int PC_WARPS = 8;
+constexpr int PC_HEADS = 8;      // heads per CTA
 constexpr int PC_MIN_TILES = 1;
+constexpr int PC_SMEM = 96 * 1024;     // two CTAs per SM
 
 __device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool zero) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -39,171 +40,255 @@ template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bflo
 }
 
 // grid (units, ceil(H / 8)); shared memory: `bufs` (1 or 2) tiles of 32 rows as stored, each row
-// 16 bytes apart from the next, and the warps' queries in fp32.  Lane r of every warp knows row r
-// of a tile; a tile is copied by 16-byte cp.async while the one before is worked on (two buffers)
-// and its rows are looked up a tile earlier still.
-// Logits: lane r of a head's warp forms the whole dot product of row r (no reduction across
-// lanes); the pitch spreads the lanes' 16-byte loads over the banks.  Values: lane i owns dims
-// 4i .. 4i+3 (+128 j).
-// Bound: latency for few rows (about 5 us: lengths, table, rows, one tile's work, the store), the
-// fp32 pipe and shared memory (two 16-byte loads for 4 or 8 products) for many.
-template <typename T>
-__global__ void __launch_bounds__(PC_WARPS * 32)
-paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
+// 16 bytes apart from the next, and the CTA's queries in fp32.  A tile is copied by 16-byte
+// cp.async while the one before is worked on (two buffers); its rows are looked up a tile earlier.
+// A warp takes HB heads and 32 / G rows of every tile (8 warps: G = 8 for up to 4 heads, 4 for 8),
+// so that each value read from shared memory meets HB heads.
+// Logits: G lanes share a row's dot products, which they exchange so that each ends with one row
+// and head.  Values: lane i owns dims 4i .. 4i+3 (+128 j) of all HB heads; narrow rows leave lanes
+// for other rows.  Each warp has its own maximum and sums; the G warps of a head meet where the
+// unit leaves the sequence.
+// Bound: latency for few rows (about 5 us: lengths, table, rows, one tile's work, the store), issue
+// slots and shared memory for many.
+template <typename T, int NO, int HB>
+__global__ void __launch_bounds__(PC_WARPS * 32, 2)
+paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
   extern __shared__ uint4 smem16[];
   __shared__ int64_t scratch[66];
+  __shared__ int rows_s[4][PC_ROWS];                  // rows of the tiles, by tile mod 4
   constexpr int VEC = Elem<T>::VEC;
   const int unit = blockIdx.x, hg = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int dk = a.dk, dv = a.dv, pitch = dk + VEC, vecs = dk / VEC;
   T* const tiles_s = reinterpret_cast<T*>(smem16);
-  float* const Qs = reinterpret_cast<float*>(tiles_s + (size_t)bufs * PC_ROWS * pitch) + (size_t)warp * dk;
-  const int h = hg * PC_WARPS + warp;
-  const bool hv = h < a.H;
-  constexpr int NO = (PC_MAXD + 127) / 128;          // groups of 4 dims per lane
+  float* const Qs = reinterpret_cast<float*>(tiles_s + (size_t)bufs * PC_ROWS * pitch);
+  const int heads = min(a.H - hg * PC_HEADS, HB * (PC_WARPS >> log_g));
+  const int hw = (warp >> log_g) * HB;                // the warp's first head, of the CTA's
+  const bool live = hw < heads;
+  const int log_r = 5 - log_g, r0 = (warp & ((1 << log_g) - 1)) << log_r;
+  const int krow = r0 + (lane & ((1 << log_r) - 1)), kpart = lane >> log_r;
+  // the lane whose logit is head u's of the warp's first row
+  auto lane_of = [](int u) { return HB == 4 ? u << 3 : 0; };
+  // lanes that copy a row, and (NO = 1) lanes that share a row's values; what is left of the warp takes other rows
+  const int log_l = vecs <= 4 ? 2 : vecs <= 8 ? 3 : vecs <= 16 ? 4 : 5;
+  const int log_v = NO > 1 || dv > 64 ? 5 : dv > 32 ? 4 : 3;
+  const int vrow = lane >> log_v, vdim = 4 * (lane & ((1 << log_v) - 1));
+  int voff[NO];                                       // (dims past the last: read, not stored)
+#pragma unroll
+  for (int i = 0; i < NO; ++i) voff[i] = vdim + 128 * i < dv ? vdim + 128 * i : 0;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // the merge waits for this grid itself
-  const PagedPlan plan = paged_plan(a, unit, threads, scratch);
-  // sequences without a row (no unit has a tile of theirs): a lane looks at each, the warp clears
-  for (int b0 = unit; b0 < a.B; b0 += 32 * a.units) {
-    const int64_t bl = (int64_t)b0 + (int64_t)lane * a.units;
-    for (unsigned none = __ballot_sync(0xffffffffu, bl < a.B && paged_tiles(a, (int)min(bl, (int64_t)a.B - 1)) == 0); none; none &= none - 1) {
-      const int b = b0 + (__ffs(none) - 1) * a.units;
-      if (!hv) continue;
-      for (int c = lane; c < dv; c += 32) Elem<T>::st((T*)a.out + ((size_t)b * a.H + h) * dv + c, 0.f);
-      if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
+  const PagedPlan plan = paged_plan(a, unit, PC_WARPS * 32, scratch);
+  // The last six warps clear the sequences without a row (no unit has a tile of theirs; a lane looks
+  // at each) and write the unit's note, while the first two look up the rows of the first tiles.
+  if (warp >= 2)
+    for (int b0 = unit; b0 < a.B; b0 += 32 * a.units) {
+      const int64_t bl = (int64_t)b0 + (int64_t)lane * a.units;
+      for (unsigned none = __ballot_sync(0xffffffffu, bl < a.B && paged_tiles(a, (int)min(bl, (int64_t)a.B - 1)) == 0); none; none &= none - 1) {
+        const int b = b0 + (__ffs(none) - 1) * a.units;
+        for (int h = hg * PC_HEADS + warp - 2; h < min(a.H, (hg + 1) * PC_HEADS); h += PC_WARPS - 2) {
+          for (int c = lane; c < dv; c += 32) Elem<T>::st((T*)a.out + ((size_t)b * a.H + h) * dv + c, 0.f);
+          if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = a.sink[h];
+        }
+      }
     }
-  }
-  if (hg == 0 && threadIdx.x == 0) paged_note(a, plan, unit);
+  if (hg == 0 && threadIdx.x == (PC_WARPS - 1) * 32) paged_note(a, plan, unit);
   PagedSeg seg;
   seg.start(plan, unit);
   while (seg.next(a)) {
     const int b = seg.b, na = seg.na, nw = seg.nw;
     const int64_t ta = seg.ta, t1 = seg.t1;
     int64_t t = seg.t0;
-    // the lane's row of a tile: in the pool or the window, -1 = none
+    // one warp looks up a tile's rows: in the pool or the window, -1 = none
     auto resolve = [&](int64_t tile) {
-      if (tile >= t1) return -1;
+      if (tile >= t1 || warp != ((int)(tile - seg.t0) & (PC_WARPS - 1))) return;
       const bool in_a = tile < ta;
-      const int64_t v = (in_a ? tile : tile - ta) * PC_ROWS + lane;
-      if (in_a) return v < na ? (int)paged_row(a, b, (int)v) : -1;
-      return v < nw ? (int)((int64_t)b * a.W + v) : -1;
+      const int v = (int)((in_a ? tile : tile - ta) * PC_ROWS) + lane;
+      rows_s[tile & 3][lane] = in_a ? (v < na ? (int)paged_row(a, b, v) : -1) : (v < nw ? b * a.W + v : -1);
     };
-    auto copy = [&](int64_t tile, int row, int buf) {
+    auto copy = [&](int64_t tile, int buf) {
+      if (tile >= t1) return;
       const T* base = tile < ta ? (const T*)a.pages : (const T*)a.win;
       T* dst = tiles_s + (size_t)buf * PC_ROWS * pitch;
-      for (int i = threadIdx.x; i < PC_ROWS * vecs; i += threads) {       // whole warps
-        const int r = i / vecs, c = (i - r * vecs) * VEC;
-        const int y = __shfl_sync(0xffffffffu, row, r);
-        cp_async16_zfill(dst + r * pitch + c, base + (size_t)(y < 0 ? 0 : y) * dk + c, y < 0);
+      for (int r = warp * (32 >> log_l) + (lane >> log_l); r < PC_ROWS; r += PC_WARPS * (32 >> log_l)) {
+        const int y = rows_s[tile & 3][r];
+        const T* src = base + (size_t)(y < 0 ? 0 : y) * dk;
+        for (int c = lane & ((1 << log_l) - 1); c < vecs; c += 1 << log_l)
+          cp_async16_zfill(dst + r * pitch + c * VEC, src + c * VEC, y < 0);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int row = resolve(t), next = resolve(t + 1);
-    copy(t, row, 0);
-    if (hv)
-      for (int c = lane * VEC; c < dk; c += 32 * VEC) {
-        float x[VEC];
-        Elem<T>::ld_vec((const T*)a.q + ((size_t)b * a.H + h) * dk + c, x);
+    resolve(t);
+    resolve(t + 1);
+    __syncthreads();
+    copy(t, 0);
+    // the queries (heads past the last: zeros), while the first rows are on their way
+    const T* qb = (const T*)a.q + ((size_t)b * a.H + hg * PC_HEADS) * dk;
+    for (int c = threadIdx.x * VEC; c < HB * (PC_WARPS >> log_g) * dk; c += PC_WARPS * 32 * VEC) {
+      float x[VEC];
 #pragma unroll
-        for (int u = 0; u < VEC; ++u) Qs[c + u] = x[u];
-      }
-    float4 o[NO];
+      for (int u = 0; u < VEC; ++u) x[u] = 0.f;
+      if (c < heads * dk) Elem<T>::ld_vec(qb + c, x);
 #pragma unroll
-    for (int i = 0; i < NO; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m_run = -INFINITY, l_run = 0.f;
+      for (int u = 0; u < VEC; u += 4) *reinterpret_cast<float4*>(Qs + c + u) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+    }
+    float4 o[HB][NO];
+#pragma unroll
+    for (int u = 0; u < HB; ++u)
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m_run = -INFINITY, l_run = 0.f;             // of the lane's head; the sum of the lane's rows
     int buf = 0;
     for (; t < t1; ++t) {
-      const bool ahead = bufs == 2 && t + 1 < t1;
-      if (ahead) copy(t + 1, next, buf ^ 1);
-      const int after = resolve(t + 2);                // its loads are in flight during the tile's work
-      if (ahead) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      else asm volatile("cp.async.wait_group 0;" ::: "memory");
-      __syncthreads();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();                                // the tile is there, and the one before is read
+      if (bufs == 2) copy(t + 1, buf ^ 1);
+      resolve(t + 2);
       const T* Ks = tiles_s + (size_t)buf * PC_ROWS * pitch;
-      if (hv) {
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-        const T* kr = Ks + lane * pitch;
-#pragma unroll 4
-        for (int c = 0; c < dk; c += VEC) {
+      if (live) {
+        float s[HB][2];
+#pragma unroll
+        for (int u = 0; u < HB; ++u) s[u][0] = s[u][1] = 0.f;
+        const T* kr = Ks + krow * pitch;
+        const float* qh = Qs + hw * dk;
+#pragma unroll 2
+        for (int c = kpart * VEC; c < dk; c += VEC << log_g) {
           float x[VEC];
           Elem<T>::ld_vec(kr + c, x);
 #pragma unroll
-          for (int u = 0; u < VEC; u += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(Qs + c + u);
-            s0 = fmaf(x[u], y.x, s0);
-            s1 = fmaf(x[u + 1], y.y, s1);
-            s2 = fmaf(x[u + 2], y.z, s2);
-            s3 = fmaf(x[u + 3], y.w, s3);
-          }
+          for (int u = 0; u < HB; ++u)
+#pragma unroll
+            for (int v = 0; v < VEC; v += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(qh + u * dk + c + v);
+              s[u][0] = fmaf(x[v], y.x, s[u][0]);
+              s[u][1] = fmaf(x[v + 1], y.y, s[u][1]);
+              s[u][0] = fmaf(x[v + 2], y.z, s[u][0]);
+              s[u][1] = fmaf(x[v + 3], y.w, s[u][1]);
+            }
         }
-        const float logit = row >= 0 ? ((s0 + s1) + (s2 + s3)) * a.sm_scale : -INFINITY;
-        const float m_new = fmaxf(m_run, warp_max(logit));
-        if (m_new != -INFINITY) {                      // else: no row of the piece so far
-          const float alpha = __expf(m_run - m_new);
-          const float p = __expf(logit - m_new);
-          l_run = l_run * alpha + warp_sum(p);
+        float dot;
+        if constexpr (HB == 4) {
+          float d[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) d[u] = s[u][0] + s[u][1];
+          const bool up = lane & 16, odd = lane & 8;  // these lanes go on with heads 2 and 3; with the odd one
+          const float e0 = (up ? d[2] : d[0]) + __shfl_xor_sync(0xffffffffu, up ? d[0] : d[2], 16);
+          const float e1 = (up ? d[3] : d[1]) + __shfl_xor_sync(0xffffffffu, up ? d[1] : d[3], 16);
+          dot = (odd ? e1 : e0) + __shfl_xor_sync(0xffffffffu, odd ? e0 : e1, 8);
+          if (log_r == 2) dot += __shfl_xor_sync(0xffffffffu, dot, 4);
+        } else {
+          dot = s[0][0] + s[0][1];
+          for (int w = 1 << log_r; w < 32; w <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
+        }
+        const float logit = rows_s[t & 3][krow] >= 0 ? dot * a.sm_scale : -INFINITY;
+        float m_new = fmaxf(m_run, logit);
+        for (int w = 1; w < 1 << log_r; w <<= 1) m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, w));
+        const float m0 = m_new == -INFINITY ? 0.f : m_new;   // no row so far: p = 0 (a NaN stays one)
+        const float p = __expf(logit - m0);
+        if (__any_sync(0xffffffffu, m_new > m_run)) {
+          const float alpha = __expf(m_run - m0);
+          l_run *= alpha;
           m_run = m_new;
 #pragma unroll
-          for (int i = 0; i < NO; ++i) { o[i].x *= alpha; o[i].y *= alpha; o[i].z *= alpha; o[i].w *= alpha; }
-#pragma unroll 4
-          for (int r = 0; r < PC_ROWS; ++r) {
-            const float pr = __shfl_sync(0xffffffffu, p, r);
-            const T* vr = Ks + r * pitch + 4 * lane;
+          for (int u = 0; u < HB; ++u) {
+            const float au = __shfl_sync(0xffffffffu, alpha, lane_of(u));
 #pragma unroll
-            for (int i = 0; i < NO; ++i) {
-              if (4 * lane + 128 * i < dv) {
-                float x[4];
-                load4<T>(vr + 128 * i, x);
-                o[i].x = fmaf(pr, x[0], o[i].x);
-                o[i].y = fmaf(pr, x[1], o[i].y);
-                o[i].z = fmaf(pr, x[2], o[i].z);
-                o[i].w = fmaf(pr, x[3], o[i].w);
-              }
+            for (int i = 0; i < NO; ++i) { o[u][i].x *= au; o[u][i].y *= au; o[u][i].z *= au; o[u][i].w *= au; }
+          }
+        }
+        l_run += p;
+#pragma unroll 2
+        for (int k = vrow; k < 1 << log_r; k += 32 >> log_v) {            // whole warps
+          float pr[HB];
+#pragma unroll
+          for (int u = 0; u < HB; ++u) pr[u] = __shfl_sync(0xffffffffu, p, lane_of(u) + k);
+          const T* vr = Ks + (r0 + k) * pitch;
+#pragma unroll
+          for (int i = 0; i < NO; ++i) {
+            float x[4];
+            load4<T>(vr + voff[i], x);
+#pragma unroll
+            for (int u = 0; u < HB; ++u) {
+              o[u][i].x = fmaf(pr[u], x[0], o[u][i].x);
+              o[u][i].y = fmaf(pr[u], x[1], o[u][i].y);
+              o[u][i].z = fmaf(pr[u], x[2], o[u][i].z);
+              o[u][i].w = fmaf(pr[u], x[3], o[u][i].w);
             }
           }
         }
       }
-      __syncthreads();                                // the buffer is read
-      row = next;
-      next = after;
-      if (bufs == 2) buf ^= 1;
-      else if (t + 1 < t1) copy(t + 1, row, 0);
-    }
-    if (!hv) continue;
-    if (seg.whole) {
-      const float sk = a.sink[h], M = fmaxf(sk, m_run);
-      float den = 0.f, f = 0.f;
-      if (M != -INFINITY) {
-        f = m_run == -INFINITY ? 0.f : __expf(m_run - M);
-        den = __expf(sk - M) + l_run * f;
+      if (bufs == 2) {
+        buf ^= 1;
+      } else {
+        __syncthreads();
+        copy(t + 1, 0);
       }
-      const float inv = den > 0.f ? f / den : 0.f;
+    }
+    __syncthreads();                                  // all tiles are read
+    // the G warps of a head meet in the tiles' memory: per warp and head {m, l, -, -, o}
+    float* const left = reinterpret_cast<float*>(smem16);
+    if (live) {
+      float* const mine = left + (size_t)warp * HB * (dv + 4);
+      for (int w = 1; w < 1 << log_r; w <<= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, w);
 #pragma unroll
-      for (int i = 0; i < NO; ++i) {
-        const int c = 4 * lane + 128 * i;
-        if (c < dv) {
-          T* dst = (T*)a.out + ((size_t)b * a.H + h) * dv + c;
-          Elem<T>::st(dst, o[i].x * inv);
-          Elem<T>::st(dst + 1, o[i].y * inv);
-          Elem<T>::st(dst + 2, o[i].z * inv);
-          Elem<T>::st(dst + 3, o[i].w * inv);
+      for (int u = 0; u < HB; ++u) {
+        if (NO == 1)                                  // the lanes of other rows
+          for (int w = 1 << log_v; w < 32; w <<= 1) {
+            o[u][0].x += __shfl_xor_sync(0xffffffffu, o[u][0].x, w);
+            o[u][0].y += __shfl_xor_sync(0xffffffffu, o[u][0].y, w);
+            o[u][0].z += __shfl_xor_sync(0xffffffffu, o[u][0].z, w);
+            o[u][0].w += __shfl_xor_sync(0xffffffffu, o[u][0].w, w);
+          }
+        if (lane == lane_of(u)) *reinterpret_cast<float2*>(mine + u * (dv + 4)) = make_float2(m_run, l_run);
+#pragma unroll
+        for (int i = 0; i < NO; ++i)
+          if (vdim + 128 * i < dv && vrow == 0) *reinterpret_cast<float4*>(mine + u * (dv + 4) + 4 + vdim + 128 * i) = o[u][i];
+      }
+    }
+    __syncthreads();
+    const int pieces = dv / 4;
+    for (int i = threadIdx.x; i < heads * pieces; i += PC_WARPS * 32) {
+      const int hh = i / pieces, c = 4 * (i - hh * pieces), h = hg * PC_HEADS + hh;
+      const float* src = left + (size_t)(((hh / HB) << log_g) * HB + hh % HB) * (dv + 4);
+      const size_t step = (size_t)HB * (dv + 4);
+      float M = -INFINITY;
+#pragma unroll 1
+      for (int g = 0; g < 1 << log_g; ++g) M = fmaxf(M, src[g * step]);
+      const float m0 = M == -INFINITY ? 0.f : M;
+      float l = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int g = 0; g < 1 << log_g; ++g) {
+        const float2 ml = *reinterpret_cast<const float2*>(src + g * step);
+        const float4 x = *reinterpret_cast<const float4*>(src + g * step + 4 + c);
+        const float w = __expf(ml.x - m0);
+        l = fmaf(w, ml.y, l);
+        y = make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
+      }
+      if (seg.whole) {
+        const float sk = a.sink[h], top = fmaxf(sk, M);
+        float den = 0.f, f = 0.f;
+        if (top != -INFINITY || l != 0.f) {
+          f = M == -INFINITY ? 0.f : __expf(M - top);
+          den = (sk == -INFINITY ? 0.f : __expf(sk - top)) + l * f;
+        }
+        const float inv = den > 0.f ? f / den : 0.f;
+        T* dst = (T*)a.out + ((size_t)b * a.H + h) * dv + c;
+        Elem<T>::st(dst, y.x * inv);
+        Elem<T>::st(dst + 1, y.y * inv);
+        Elem<T>::st(dst + 2, y.z * inv);
+        Elem<T>::st(dst + 3, y.w * inv);
+        if (a.lse && c == 0) a.lse[(size_t)b * a.H + h] = den == 0.f ? -INFINITY : top + logf(den);
+      } else {
+        float* blk = a.part + (size_t)seg.slot(unit) * paged_part_block(a.H, dv);
+        *reinterpret_cast<float4*>(blk + paged_part_val(a.H, h, c)) = y;
+        if (c == 0) {
+          float4* rec = reinterpret_cast<float4*>(blk + paged_part_rec(a.H, dv, h));
+          rec[0] = make_float4(M, l, 1.f, 1.f);
+          rec[1] = make_float4(1.f, 1.f, 0.f, 0.f);
         }
       }
-      if (a.lse && lane == 0) a.lse[(size_t)b * a.H + h] = den > 0.f ? M + logf(den) : -INFINITY;
-    } else {
-      float* blk = a.part + (size_t)seg.slot(unit) * paged_part_block(a.H, dv);
-#pragma unroll
-      for (int i = 0; i < NO; ++i) {
-        const int c = 4 * lane + 128 * i;
-        if (c < dv) *reinterpret_cast<float4*>(blk + paged_part_val(a.H, h, c)) = o[i];
-      }
-      if (lane == 0) {
-        float4* rec = reinterpret_cast<float4*>(blk + paged_part_rec(a.H, dv, h));
-        rec[0] = make_float4(m_run, l_run, 1.f, 1.f);
-        rec[1] = make_float4(1.f, 1.f, 0.f, 0.f);
-      }
     }
+    __syncthreads();                                  // the next segment's tiles may land
   }
 }
 
@@ -217,6 +302,7 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs) {
 // the latency of its few round trips.
 constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 5, PM_PER_SM = 2;
 constexpr int PM_FEW = 8;        // partials that one warp joins by itself
+constexpr int PM_ROUNDS = 2;     // notes of a thread: up to 512 units
 // Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)
 constexpr size_t pm_unit_bytes(bool part16) { return PM_H * (sizeof(float4) + (part16 ? sizeof(float2) : 0)) + sizeof(int4); }
 // acc += w times a 16-byte piece of a partial
@@ -255,30 +341,42 @@ paged_merge_kernel(PagedAttnArgs a) {
   float2* const s23 = reinterpret_cast<float2*>(wts + (size_t)a.units * PM_H);
   __shared__ float red[2][PM_THREADS / 32][PM_H];
   __shared__ float sums[V][PM_THREADS];
-  __shared__ int counts[2];
+  __shared__ int counts[PM_ROUNDS * PM_THREADS / 32];
   const int dv = a.dv, H = a.H;
   const int hl = threadIdx.x & (PM_H - 1), j = threadIdx.x / PM_H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the list: sequences of few partials from the front, the others from the back
-  if (warp == 0) {
-    const int2* notes = paged_notes(a);
-    int few = 0, many = 0;
-#pragma unroll 1
-    for (int u0 = 0; u0 < a.units; u0 += 32) {
-      const int2 note = u0 + lane < a.units ? __ldcg(&notes[u0 + lane]) : make_int2(-1, 0);
-      const unsigned f = __ballot_sync(0xffffffffu, note.y > 0 && note.y <= PM_FEW), m = __ballot_sync(0xffffffffu, note.y > PM_FEW);
-      const unsigned below = (1u << lane) - 1u;
-      if (note.y > 0)
-        list[note.y <= PM_FEW ? few + __popc(f & below) : a.units - 1 - many - __popc(m & below)] =
-            make_int4(u0 + lane, note.x, note.y, 0);
-      few += __popc(f);
-      many += __popc(m);
-    }
-    if (lane == 0) { counts[0] = few; counts[1] = many; }
+  // the list: sequences of few partials from the front, the others from the back; the same in every CTA
+  int few[PM_ROUNDS], many[PM_ROUNDS];               // of the lanes below this one
+  int2 note[PM_ROUNDS];
+#pragma unroll
+  for (int r = 0; r < PM_ROUNDS; ++r) {
+    const int u = r * PM_THREADS + threadIdx.x;
+    note[r] = u < a.units ? __ldcg(&paged_notes(a)[u]) : make_int2(-1, 0);
+  }
+#pragma unroll
+  for (int r = 0; r < PM_ROUNDS; ++r) {
+    const unsigned f = __ballot_sync(0xffffffffu, note[r].y > 0 && note[r].y <= PM_FEW), m = __ballot_sync(0xffffffffu, note[r].y > PM_FEW);
+    few[r] = __popc(f & ((1u << lane) - 1u));
+    many[r] = __popc(m & ((1u << lane) - 1u));
+    if (lane == 0) counts[r * (PM_THREADS / 32) + warp] = __popc(f) | __popc(m) << 16;
   }
   __syncthreads();
-  const int count = counts[1];
+  int all = 0;                                        // few in the low half, many in the high one
+#pragma unroll
+  for (int r = 0; r < PM_ROUNDS; ++r) {
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < PM_THREADS / 32; ++w) {
+      if (w == warp) before = all;
+      all += counts[r * (PM_THREADS / 32) + w];
+    }
+    if (note[r].y > 0)
+      list[note[r].y <= PM_FEW ? (before & 0xffff) + few[r] : a.units - 1 - (before >> 16) - many[r]] =
+          make_int4(r * PM_THREADS + threadIdx.x, note[r].x, note[r].y, 0);
+  }
+  __syncthreads();
+  const int n_few = all & 0xffff, count = all >> 16;
   const int hb = (H + PM_H - 1) / PM_H, pieces = dv / V;
   int slices = 1;
   while (slices < PM_SLICES && 2 * count * hb * slices <= (int)gridDim.x && pieces / slices > 4) slices <<= 1;
@@ -288,7 +386,7 @@ paged_merge_kernel(PagedAttnArgs a) {
     // Few partials: a warp takes eight heads and 8 pieces of the dims.  Lane (head, q): partials q and
     // q + 4 in the weights, pieces q and q + 4 in the sums; all loads are one round trip.
     const int q = lane >> 3, wide = (pieces + 7) / 8;
-    for (int item = blockIdx.x * (PM_THREADS / 32) + warp; item < counts[0] * hb * wide; item += gridDim.x * (PM_THREADS / 32)) {
+    for (int item = blockIdx.x * (PM_THREADS / 32) + warp; item < n_few * hb * wide; item += gridDim.x * (PM_THREADS / 32)) {
       const int cg = item % wide, blk8 = item / wide % hb;
       const int4 cut = list[item / (wide * hb)];
       const int b = cut.y, n = cut.z, h = blk8 * PM_H + hl;
@@ -296,15 +394,18 @@ paged_merge_kernel(PagedAttnArgs a) {
       const int hc = hv ? h : H - 1;
       const float* part = a.part + (size_t)(2 * cut.x) * block;
       auto partial = [&](int p) { return part + (p ? 2 * p * block : block); };
-      uint4 x[2][PM_FEW];
+      uint4 x[2][4];                                  // four partials' pieces; the first four's are on their way
+      auto load = [&](int p0) {
 #pragma unroll
-      for (int u = 0; u < PM_FEW; ++u) {
+        for (int u = 0; u < 4; ++u) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = cg * 8 + 4 * k + q;
-          if (u < n && c < pieces) x[k][u] = __ldcg(reinterpret_cast<const uint4*>(partial(u)) + (size_t)c * H + hc);
+          for (int k = 0; k < 2; ++k) {
+            const int c = cg * 8 + 4 * k + q;
+            if (p0 + u < n && c < pieces) x[k][u] = __ldcg(reinterpret_cast<const uint4*>(partial(p0 + u)) + (size_t)c * H + hc);
+          }
         }
-      }
+      };
+      load(0);
       const size_t rec = paged_part_rec(H, dv, hc);
       const float sk = a.sink[hc];
       float m[2], l[2], w[2];
@@ -340,12 +441,16 @@ paged_merge_kernel(PagedAttnArgs a) {
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int u = 0; u < V; ++u) acc[k][u] = 0.f;
+#pragma unroll 1
+      for (int p0 = 0; p0 < n; p0 += 4) {
+        if (p0) load(p0);
 #pragma unroll
-      for (int u = 0; u < PM_FEW; ++u) {
-        if (u < n) {
-          const float wu = __shfl_sync(0xffffffffu, w[u >> 2], hl + 8 * (u & 3)) * inv;
+        for (int u = 0; u < 4; ++u) {
+          if (p0 + u < n) {
+            const float wu = __shfl_sync(0xffffffffu, p0 ? w[1] : w[0], hl + 8 * u) * inv;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) merge_add<PART16>(acc[k], x[k][u], wu);
+            for (int k = 0; k < 2; ++k) merge_add<PART16>(acc[k], x[k][u], wu);
+          }
         }
       }
 #pragma unroll
@@ -353,7 +458,7 @@ paged_merge_kernel(PagedAttnArgs a) {
         const int c = cg * 8 + 4 * k + q;
         if (hv && c < pieces) merge_store<T, V>((T*)a.out + ((size_t)b * H + h) * dv + V * c, acc[k]);
       }
-      if (a.lse && cg == 0 && q == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+      if (a.lse && cg == 0 && q == 0 && hv) a.lse[(size_t)b * H + h] = den == 0.f ? -INFINITY : M + logf(den);
     }
   }
   int gw = PM_C;                                      // threads along a slice; the other PM_C / gw share its partials
@@ -453,7 +558,7 @@ paged_merge_kernel(PagedAttnArgs a) {
         merge_store<T, V>((T*)a.out + ((size_t)b * H + h) * dv + V * c, acc);
       }
     }
-    if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+    if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den == 0.f ? -INFINITY : M + logf(den);
     __syncthreads();                                  // the weights and sums are read
   }
 }
@@ -461,6 +566,7 @@ paged_merge_kernel(PagedAttnArgs a) {
 }  // namespace
 
 cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, cudaStream_t st) {
+  if (a.units > PM_ROUNDS * PM_THREADS) return cudaErrorInvalidConfiguration;
   if (a.units == 1) return cudaSuccess;                // nothing is ever cut
   const int64_t most = (int64_t)(a.units - 1) * ((a.H + PM_H - 1) / PM_H) * PM_SLICES;
   const int grid = PM_PER_SM * num_sms();
@@ -482,7 +588,7 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, c
 
 // Two CTAs per SM over the head groups.
 int paged_units_cc(int B, int H, int64_t rows_max) {
-  const int groups = (H + PC_WARPS - 1) / PC_WARPS;
+  const int groups = (H + PC_HEADS - 1) / PC_HEADS;
   return paged_units(2 * num_sms() / groups, B, rows_max, PC_ROWS, PC_MIN_TILES);
 }
 
@@ -492,17 +598,27 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
   a.min_tiles = PC_MIN_TILES;
   a.begin_cost = 0;
   a.units = paged_units(a, paged_units_cc(a.B, a.H, paged_rows_max(a)));
-  const int warps = a.H < PC_WARPS ? a.H : PC_WARPS;
+  // Heads of a warp: 4 share each value read; 1 where that would leave warps' lanes to heads that are
+  // not there (48 x 4000 rows of 64 dims in fp32: one head 28.5 us against 31.2 the other way, two
+  // heads 28.8 against 31.1)
+  const int hb = a.H <= 2 ? 1 : 4;
+  int log_g = 3;                                      // warps of a head: the 8 over the CTA's heads
+  while (log_g > 0 && (hb << (3 - log_g)) < (a.H < PC_HEADS ? a.H : PC_HEADS)) --log_g;
   auto go = [&](auto tag) {
     using T = decltype(tag);
-    const size_t tile = (size_t)PC_ROWS * (a.dk + Elem<T>::VEC) * sizeof(T), qs = (size_t)warps * a.dk * sizeof(float);
-    const int bufs = 2 * tile + qs <= 48 * 1024 ? 2 : 1;      // two only while several CTAs still share an SM
-    const dim3 grid(a.units, (a.H + PC_WARPS - 1) / PC_WARPS);
-    static std::atomic<uint64_t> ready;
-    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(paged_attn_cc_kernel<T>), ready, 96 * 1024);
+    const size_t tile = (size_t)PC_ROWS * (a.dk + Elem<T>::VEC) * sizeof(T), qs = (size_t)PC_HEADS * a.dk * sizeof(float);
+    // One buffer holds the warps' results in fp32 where the warps of all heads meet; in bf16 it takes
+    // two, and two always fit.
+    const int bufs = 2 * tile + qs <= PC_SMEM ? 2 : 1;
+    const dim3 grid(a.units, (a.H + PC_HEADS - 1) / PC_HEADS);
+    const int no = a.dv <= 128 ? 0 : a.dv <= 512 ? 1 : 2, at = hb == 1 ? no : 3 + no;
+    void (*const kerns[])(PagedAttnArgs, int, int) = {paged_attn_cc_kernel<T, 1, 1>, paged_attn_cc_kernel<T, 4, 1>, paged_attn_cc_kernel<T, 5, 1>,
+                                                      paged_attn_cc_kernel<T, 1, 4>, paged_attn_cc_kernel<T, 4, 4>, paged_attn_cc_kernel<T, 5, 4>};
+    static std::atomic<uint64_t> ready[6];
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kerns[at]), ready[at], PC_SMEM);
     if (e != cudaSuccess) return e;
     note_launch();
-    paged_attn_cc_kernel<T><<<grid, warps * 32, bufs * tile + qs, st>>>(a, bufs);
+    kerns[at]<<<grid, PC_WARPS * 32, bufs * tile + qs, st>>>(a, bufs, log_g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_paged_merge(a, dtype, false, st);

@@ -576,7 +576,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         }
       }
       __syncwarp();
-      if (hv && wg == 0 && half == 0 && seg.whole && a.lse) a.lse[(size_t)seg.b * a.H + h] = den > 0.f ? M + logf(den) : -INFINITY;
+      if (hv && wg == 0 && half == 0 && seg.whole && a.lse) a.lse[(size_t)seg.b * a.H + h] = den == 0.f ? -INFINITY : M + logf(den);
     }
     if (!ok) atomicExch(&sm.abort_flag, 1);
   }

@@ -557,3 +557,25 @@ def test_append_with_strides_that_mean_nothing():
     torch.cuda.synchronize()
     check_rotated(q[0, :, 512:], q_pe[0], entry, inv, True, "single")
     assert torch.equal(pages[table[0, 0].long(), 9, :512], rows[0, :512])
+
+
+@pytest.mark.parametrize("dtype,H,dk,dv", [(BF, 128, 576, 512), (BF, 7, 576, 512), (F32, 4, 64, 64), (F32, 1, 64, 36), (F32, 11, 72, 64)])
+@pytest.mark.parametrize("every", [False, True])
+def test_a_nan_that_is_attended_shows_and_stays_with_its_sequence(dtype, H, dk, dv, every):
+    c = Case(113, dtype, H, dk, dv, 16, [40, 900, 40], 9)
+    for e in range(900) if every else [517]:
+        c.pages[c.table[1, e // 16].long(), e % 16] = math.nan
+    if every:
+        c.win[1] = math.nan
+    c.call()
+    torch.cuda.synchronize()
+    assert csa.read_device_error() == 0
+    assert bool(c.out[1].isnan().all()) and bool(c.lse[1].isnan().all())
+    for b in (0, 2):
+        check(c.out[b:b + 1], c.lse[b:b + 1], c.q[b:b + 1], lambda _, b=b: c.rows_of(b), c.sink, c.scale)
+
+
+@pytest.mark.parametrize("H", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("dtype,dk,dv", [(F32, 64, 64), (F32, 8, 4), (BF, 136, 100), (F32, 576, 576), (BF, 64, 16), (F32, 320, 260)])
+def test_few_heads_share_a_tile_s_rows(H, dtype, dk, dv):
+    Case(127 + H, dtype, H, dk, dv, 24, [0, 1, 31, 33, 700, 4100], 9).run_and_check()
