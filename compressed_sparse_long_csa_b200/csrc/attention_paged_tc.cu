@@ -80,6 +80,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 32 bytes by one store: a whole sector (`wide`: the address is a multiple of 32), or two of 16
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w, bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+  else
+    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
 // 2^x by the MUFU.EX2 unit (relative error about 2^-22)
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
@@ -380,6 +388,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       return __all_sync(0xffffffffu, tc::mbar_wait(&sm.segb, met++ & 1));
     };
     // logits in the base-2 domain: P = 2^(s - m)
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     const float scale2 = a.sm_scale * 1.4426950408889634f;
     const float scale = fmaxf(fabsf(scale2), 1.2e-38f);          // not 0: an absent row's -inf must stay one
     bool ok = true;
@@ -557,18 +566,25 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         if (!hv) continue;
         __nv_bfloat16* o = (__nv_bfloat16*)a.out + ((size_t)seg.b * a.H + h) * 512 + d0 + c * 64;
         uint4* p16 = reinterpret_cast<uint4*>(blk) + (size_t)((d0 + c * 64) / 8) * a.H + h;
+        if (seg.whole) {
+          // each lane has a row of its own: whole sectors, or the store's lines cost as much again
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float f8[8];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f8[j] = __uint_as_float(v[q * 8 + j]) * f;
-          if (seg.whole) {
-            Elem<__nv_bfloat16>::st_vec(o + q * 8, f8);
-          } else {
+            for (int j = 0; j < 8; ++j) {
+              const __nv_bfloat162 bf = __floats2bfloat162_rn(__uint_as_float(v[q * 16 + 2 * j]) * f, __uint_as_float(v[q * 16 + 2 * j + 1]) * f);
+              w[j] = *reinterpret_cast<const uint32_t*>(&bf);
+            }
+            st_global32(o + q * 16, w, wide);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const __half2 hf = __floats2half2_rn(f8[2 * j], f8[2 * j + 1]);
+              const __half2 hf = __floats2half2_rn(__uint_as_float(v[q * 8 + 2 * j]) * f, __uint_as_float(v[q * 8 + 2 * j + 1]) * f);
               w[j] = *reinterpret_cast<const uint32_t*>(&hf);
             }
             p16[(size_t)q * a.H] = make_uint4(w[0], w[1], w[2], w[3]);

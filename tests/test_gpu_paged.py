@@ -579,3 +579,18 @@ def test_a_nan_that_is_attended_shows_and_stays_with_its_sequence(dtype, H, dk, 
 @pytest.mark.parametrize("dtype,dk,dv", [(F32, 64, 64), (F32, 8, 4), (BF, 136, 100), (F32, 576, 576), (BF, 64, 16), (F32, 320, 260)])
 def test_few_heads_share_a_tile_s_rows(H, dtype, dk, dv):
     Case(127 + H, dtype, H, dk, dv, 24, [0, 1, 31, 33, 700, 4100], 9).run_and_check()
+
+
+def test_out_and_rows_at_16_bytes():
+    """Every address a multiple of 16 bytes, none of 32."""
+    c = Case(131, BF, 128, 576, 512, 64, [100, 0, 9000, 64], 9)
+
+    def moved(t):
+        buf = torch.empty(t.numel() + 16, device="cuda", dtype=t.dtype)
+        k = 16 // t.element_size()
+        v = buf[k:k + t.numel()].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+    c.q, c.pages, c.win, c.out, c.lse, c.sink, c.ws = (moved(t) for t in (c.q, c.pages, c.win, c.out, c.lse, c.sink, c.ws))
+    c.run_and_check()
