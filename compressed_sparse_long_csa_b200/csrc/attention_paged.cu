@@ -21,7 +21,7 @@ namespace {
 constexpr int PC_ROWS = 32;      // rows per tile: one lane per row in the logits
 constexpr int PC_WARPS = 8;
 constexpr int PC_HEADS = 8;      // heads per CTA
-constexpr int PC_MIN_TILES = 1;
+constexpr int PC_MIN_TILES = 1;  // (2: five sequences of up to 3001 rows of 64 dims 11.2 -> 13.5 us)
 constexpr int PC_SMEM = 96 * 1024;     // two CTAs per SM
 
 __device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool zero) {
@@ -40,7 +40,7 @@ template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bflo
 }
 
 // grid (units, ceil(H / 8)); shared memory: `bufs` (1 or 2) tiles of 32 rows as stored, each row
-// 16 bytes apart from the next, and the CTA's queries in fp32.  A tile is copied by 16-byte
+// 16 bytes longer than it need be (lanes' loads spread over the banks), and the CTA's queries in fp32.  A tile is copied by 16-byte
 // cp.async while the one before is worked on (two buffers); its rows are looked up a tile earlier.
 // A warp takes HB heads and 32 / G rows of every tile (8 warps: G = 8 for up to 4 heads, 4 for 8),
 // so that each value read from shared memory meets HB heads.
@@ -48,8 +48,9 @@ template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bflo
 // and head.  Values: lane i owns dims 4i .. 4i+3 (+128 j) of all HB heads; narrow rows leave lanes
 // for other rows.  Each warp has its own maximum and sums; the G warps of a head meet where the
 // unit leaves the sequence.
-// Bound: latency for few rows (about 5 us: lengths, table, rows, one tile's work, the store), issue
-// slots and shared memory for many.
+// Bound: latency for few rows (5.7 us for one tile: schedule 1.3, lookups and rows 2, its work 1,
+// the warps' meeting and the store 1.4), issue slots and shared memory for many (48 x 4000 rows of 64
+// dims in fp32: 4 heads 31 us, 16 heads 50; with a head per warp, 57 and 144).
 template <typename T, int NO, int HB>
 __global__ void __launch_bounds__(PC_WARPS * 32, 2)
 paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
@@ -298,9 +299,13 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
 // slice of the dims), the slices as narrow as it takes to give every CTA an item.  Eight
 // heads' 16-byte pieces of a partial are one 128-byte line.  Where a slice leaves threads
 // over, they share its pieces.  All sums run in a fixed order, so a result does not depend
-// on the order in which the units ended.  Bound: L2, H * (dv + 4) * 4 bytes per piece, and
-// the latency of its few round trips.
-constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16, PM_EARLY = 5, PM_PER_SM = 2;
+// on the order in which the units ended.  Bound: latency (the notes, the records, the partials:
+// three round trips and the launch, 4 to 6 us behind the attention) and the L2, H * (2 or 4 dv +
+// 32) bytes per piece.  Sequences of few partials are a warp's work, so that many of them run at
+// once (32 ragged sequences 109.5 us without, 106.3 with; sparse, 48 sequences 58.7 against 55.9).
+constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16;
+constexpr int PM_EARLY = 5;      // partials on their way at once (9: 64 heads 73.4 -> 73.9 us)
+constexpr int PM_PER_SM = 2;     // (1: 32 ragged sequences 105.0 -> 107.5 us)
 constexpr int PM_FEW = 8;        // partials that one warp joins by itself
 constexpr int PM_ROUNDS = 2;     // notes of a thread: up to 512 units
 // Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)
@@ -608,7 +613,7 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
     using T = decltype(tag);
     const size_t tile = (size_t)PC_ROWS * (a.dk + Elem<T>::VEC) * sizeof(T), qs = (size_t)PC_HEADS * a.dk * sizeof(float);
     // One buffer holds the warps' results in fp32 where the warps of all heads meet; in bf16 it takes
-    // two, and two always fit.
+    // two, and two always fit.  (One for fp32 too: the sequences above 11.2 -> 11.5 us.)
     const int bufs = 2 * tile + qs <= PC_SMEM ? 2 : 1;
     const dim3 grid(a.units, (a.H + PC_HEADS - 1) / PC_HEADS);
     const int no = a.dv <= 128 ? 0 : a.dv <= 512 ? 1 : 2, at = hb == 1 ? no : 3 + no;

@@ -18,6 +18,15 @@
 // and S 128 lanes x 32 columns, so lane l and lane l + 64 hold halves of the same head.
 // At a segment's end O is normalised and stored, or left as a partial for the merge.
 // Every wait is bounded (CSA_DEVERR_TIMEOUT).
+//
+// Bound: at 64 heads HBM (two sequences of 131 072 rows: 73.6 us, 3.9 TB/s of 6.56 measured; a
+// CTA's two stages keep 144 KB in flight or at work), at 128 heads the operands that the MMAs of
+// two CTAs read from shared memory, 378 KB of 128 bytes a clock per tile and CTA (32 ragged
+// sequences: 105 us, 670 TFLOP/s), for gathered rows the gathers beside them (48 x 1152 rows:
+// 54.4 us, 2.5 us a tile), for one sequence latency (100 rows: 11.6 us).  A tile's chain is load
+// 0.65 us, S 0.55 + 0.15, softmax 0.4 + 0.25, hand-over 0.2, PV 0.65; two tiles overlap.
+// Why 64 heads a CTA: O of 128 heads (512 columns) would leave no TMEM for S.  Why two bf16
+// parts of P: one part took 64 heads from 80 to 76 us when that was tried, for the error above.
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -38,7 +47,7 @@ constexpr int PT_SW = 8;                 // the warp of the queries and S
 constexpr int PT_PVW = 9;                // the warp of PV
 constexpr int PT_LDW = 10;               // first loader warp
 constexpr int PT_THREADS = PT_LDW * 32 + PT_LDT;
-constexpr int PT_MIN_TILES = 2;
+constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 12.6 us in one unit, 14.5 in two and a merge)
 constexpr int PT_BEGIN_COST = 2;         // (1: ragged batch 109.0 us, 2: 106.7, 3: 108.5)
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
