@@ -353,6 +353,8 @@ def latent_append_paged(rows, entry, pages, block_table, seq=None, pos=None, inv
     rotary parts q_pe [T, H, d_r] rotated into the last d_r values of q [T, H, d_q].  rows and q_pe may
     be strided in all but their last dimension.  See csa.h."""
     name = "latent_append_paged"
+    if rows is None or entry is None or pages is None or block_table is None:
+        raise CsaError(f"{name}: rows, entry, pages and block_table are needed")
     di = _paged(name, pages, block_table)
     n_pages, page, d = pages.shape
     B, width = block_table.shape
@@ -404,6 +406,8 @@ def attn_decode_paged_workspace_size(B, H, d_v, rows_max):
 
 
 def _paged_attn(name, call, q, pages, block_table, sel, sparse, win, win_len, sink, sm_scale, d_v, out, lse, workspace, stream):
+    if q is None or pages is None or block_table is None or sel is None or sink is None or out is None:
+        raise CsaError(f"{name}: q, pages, block_table, {'idx' if sparse else 'n_entries'}, sink and out are needed")
     di = _paged(name, pages, block_table)
     n_pages, page, d_k = pages.shape
     B, width = block_table.shape

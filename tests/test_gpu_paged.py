@@ -594,3 +594,36 @@ def test_out_and_rows_at_16_bytes():
         return v
     c.q, c.pages, c.win, c.out, c.lse, c.sink, c.ws = (moved(t) for t in (c.q, c.pages, c.win, c.out, c.lse, c.sink, c.ws))
     c.run_and_check()
+
+
+@pytest.mark.parametrize("dtype,H,dk,dv", [(BF, 128, 576, 512), (F32, 4, 64, 64)])
+def test_the_largest_pages_windows_and_selections(dtype, H, dk, dv):
+    Case(137, dtype, H, dk, dv, 65536, [70001, 5], 4096).run_and_check("dense")
+    g = gen(139)
+    idx = torch.randint(-1, 5000, (2, 65536), generator=g, device="cuda", dtype=torch.int32)
+    Case(149, dtype, H, dk, dv, 100, [5000, 5000], 4096, idx=idx).run_and_check("sparse")
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(BF, 576, 512), (F32, 64, 64)])
+def test_the_most_sequences(dtype, dk, dv):
+    """65 535 sequences of one row or none, pages of one row; out and lse have closed forms."""
+    g, B = gen(151), 65535
+    pages = randn(g, 3000, 1, dk, dtype=dtype)
+    table = torch.randint(0, 3000, (B, 1), generator=g, device="cuda", dtype=torch.int32)
+    n = (torch.arange(B, device="cuda") % 3 != 1).to(torch.int32)
+    q, sink, scale = randn(g, B, 1, dk, dtype=dtype), randn(g, 1), dk ** -0.5
+    out, lse = torch.full((B, 1, dv), 7.0, device="cuda", dtype=dtype), torch.full((B, 1), 7.0, device="cuda")
+    ws = torch.empty(csa.attn_decode_paged_workspace_size(B, 1, dv, 1), dtype=torch.uint8, device="cuda")
+    csa.hca_attn_decode_paged(q, pages, table, n, None, None, sink, scale, dv, out, lse, ws)
+    torch.cuda.synchronize()
+    assert csa.read_device_error() == 0
+    rows = pages.double()[table[:, 0].long(), 0]
+    qr = q.double()[:, 0] * rows
+    l = torch.where(n > 0, qr.sum(1) * scale, -math.inf)
+    D = (qr.abs().sum(1) * scale) * (dk + 8) * 2 * U + l.abs().nan_to_num(0, 0, 0) * 2 * U + 2.0 ** -21
+    L = torch.logaddexp(l, sink.double())
+    p = (l - L).exp()
+    want = p[:, None] * rows[:, :dv]
+    tol = (p[:, None] * rows[:, :dv].abs()) * (2 * D + 2.0 ** -15 + 2.0 ** -11 * (dtype == BF) + 40 * U)[:, None] + R[dtype] * want.abs()
+    assert bool(((out[:, 0].double() - want).abs() <= tol).all())
+    assert bool(((lse[:, 0].double() - L).abs() <= D + 40 * U + L.abs() * 2 * U).all())

@@ -86,3 +86,15 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(csa.CsaError, match="current CUDA device"):
         csa.sparse_attn_decode_paged(torch.zeros(2, 4, 64), pages, table, torch.zeros(2, 3, dtype=torch.int32), None, None,
                                      torch.zeros(4), 0.1, 64, torch.zeros(2, 4, 64))
+
+
+@pytest.mark.parametrize("missing", range(4))
+def test_binding_names_what_is_missing(missing):
+    args = [torch.zeros(2, 64), torch.zeros(2, dtype=torch.int32), torch.zeros(4, 16, 64), torch.zeros(2, 2, dtype=torch.int32)]
+    args[missing] = None
+    with pytest.raises(csa.CsaError, match="needed"):
+        csa.latent_append_paged(*args)
+    with pytest.raises(csa.CsaError, match="needed"):
+        csa.hca_attn_decode_paged(*args, None, None, torch.zeros(4), 0.1, 64, torch.zeros(2, 4, 64))
+    with pytest.raises(csa.CsaError, match="needed"):
+        csa.sparse_attn_decode_paged(*[torch.zeros(2, 4, 64)] * 4, None, None, None, 0.1, 64, torch.zeros(2, 4, 64))
