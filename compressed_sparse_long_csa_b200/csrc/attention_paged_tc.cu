@@ -51,19 +51,21 @@ constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 12.6 us i
 constexpr int PT_BEGIN_COST = 2;         // (1: ragged batch 109.0 us, 2: 106.7, 3: 108.5)
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
-constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;    // TMEM columns: O 256, S 2 x 32
+constexpr int PT_QT = 6;                 // atoms of the queries that live in TMEM
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320, TM_COLS = 512;    // TMEM columns: O 256, S 2 x 32, queries 6 x 32
 static_assert(PT_THREADS == 512, "16 warps: 128 registers a thread");
 
 struct PtSmem {
-  uint8_t q[PT_ATOMS][PT_HC * 128];          // 72 KB
-  uint8_t kv[2][PT_ATOMS][ATOM];             // 144 KB
+  uint8_t q[PT_ATOMS - PT_QT][PT_HC * 128];  // 24 KB
+  uint8_t lo[2][PT_LO][ATOM];                // 64 KB: dims 0-255 of two tiles
+  uint8_t hi[3][PT_ATOMS - PT_LO][ATOM];     // 120 KB: dims 256-575 of three
   uint8_t p[PT_HC * 128];                    // P_hi: 64 heads x 64 rows bf16; between segments the row sums
   float smax[2][2][128];                     // per tile parity and warpgroup: the lanes' tile maxima
   alignas(16) int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
   uint32_t vmask[4][2];                      // per tile mod 4 (the loader's warps may be three tiles ahead of the
                                              // softmax): bit j of word j / 32 set when row j exists
-  uint64_t full[2][2], empty[2][2];          // per stage and half of the dims (0-255, 256-575)
-  uint64_t sfull[2];
+  uint64_t lo_full[2], lo_empty[2], hi_full[3], hi_empty[3];
+  uint64_t sfull[2], sfree[2];
   uint64_t pfull, pdone, qfull, qfree, ofree, drain[2];
   uint64_t headb[2], segb;                   // softmax warps: the four of the same heads; all eight
   uint32_t tmem_base;
@@ -106,6 +108,15 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // byte offset of 16-byte chunk c of row j in a 128-byte-swizzled atom
 __device__ __forceinline__ uint32_t sw128_off(int j, int c) { return (j >> 3) * 1024 + (j & 7) * 128 + ((c ^ (j & 7)) << 4); }
 
+// A place in a ring of slots and its phase.
+struct RingPos {
+  int at;
+  uint32_t ph;
+  __device__ __forceinline__ void step(int n) {
+    if (++at == n) { at = 0; ph ^= 1; }
+  }
+};
+
 template <bool SPARSE>
 __global__ void __launch_bounds__(PT_THREADS, 1)
 paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant__ PagedAttnArgs a, int halves, int box) {
@@ -115,12 +126,15 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   const int unit = blockIdx.x / halves, hh = blockIdx.x - unit * halves;
 
   if (threadIdx.x == 0) {
+    for (int s = 0; s < 3; ++s) {
+      tc::mbar_init(&sm.hi_full[s], 1);
+      tc::mbar_init(&sm.hi_empty[s], 1);
+    }
     for (int s = 0; s < 2; ++s) {
-      for (int x = 0; x < 2; ++x) {
-        tc::mbar_init(&sm.full[s][x], 1);
-        tc::mbar_init(&sm.empty[s][x], 1);
-      }
+      tc::mbar_init(&sm.lo_full[s], 1);
+      tc::mbar_init(&sm.lo_empty[s], 1);
       tc::mbar_init(&sm.sfull[s], 1);
+      tc::mbar_init(&sm.sfree[s], PT_SMW);
       tc::mbar_init(&sm.drain[s], 1);
     }
     tc::mbar_init(&sm.pfull, PT_SMW);
@@ -152,14 +166,14 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     // waited for where it is issued.
     const int lg = threadIdx.x - PT_LDW * 32;
     struct Row {
-      bool is, in_a;                                  // a tile of the unit; of the entries (else of the window)
+      bool is, in_a, first;                           // a tile of the unit; of the entries (else of the window); of its segment
       int b, e, id;                                   // sequence; entry (or the window's row), -1 = none; page id
     };
     int64_t t = 0;
     bool more = seg.next(a);
     if (more) t = seg.t0;
     auto entry_of = [&]() {                           // the next tile: the entry
-      Row r{more, t < seg.ta, seg.b, -1, 0};
+      Row r{more, t < seg.ta, t == seg.t0, seg.b, -1, 0};
       if (!more) return r;
       if (lg < PT_ROWS) {
         const int64_t v = (r.in_a ? t : t - seg.ta) * PT_ROWS + lg;
@@ -186,11 +200,31 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     Row now = entry_of(), next = entry_of(), after = entry_of();
     now = page_of(now);
     next = page_of(next);
-    int n_lo = 0, n_hi = 0;                           // tile halves started (for the drain)
+    RingPos lo{0, 0}, hi{0, 0};                       // the next slot of each ring
+    int n_lo = 0, n_hi = 0;                           // slots started (for the drain)
+    auto half_free = [&](int x) { return x ? tc::mbar_wait(&sm.hi_empty[hi.at], hi.ph ^ 1) : tc::mbar_wait(&sm.lo_empty[lo.at], lo.ph ^ 1); };
+    auto half_full = [&](int x) { return x ? &sm.hi_full[hi.at] : &sm.lo_full[lo.at]; };
+    auto atom_of = [&](int at) { return at < PT_LO ? sm.lo[lo.at][at] : sm.hi[hi.at][at - PT_LO]; };
+    static_assert(PT_QT == PT_LDT / 32 && PT_ATOMS - PT_LO <= PT_LDT / 32, "an atom a warp");
     for (int i = 0; now.is; ++i) {
+      bool in_time = true;
+      if (now.first) {
+        // a segment's first slots bring the queries' atoms for TMEM, an atom a warp
+        const int at = lg >> 5;
+        if (lane == 0) {
+          in_time = half_free(at >= PT_LO);
+          if (at == 0) tc::mbar_arrive_expect_tx(half_full(0), PT_LO * ATOM);
+          if (at == PT_LO) tc::mbar_arrive_expect_tx(half_full(1), (PT_QT - PT_LO) * ATOM);
+          if (in_time) tc::tma_load_2d(atom_of(at), &maps.q, half_full(at >= PT_LO), 64 * at, now.b * a.H + hh * PT_HC);
+        }
+        in_time = __shfl_sync(0xffffffffu, in_time, 0);
+        ++n_lo;
+        ++n_hi;
+        lo.step(2);
+        hi.step(3);
+      }
       const int st = i & 1, y = row_of(now);
       const bool in_a = now.in_a;
-      const uint32_t ph = ((i >> 1) & 1) ^ 1;
       // what needs no free stage comes first: the rows, which of them exist, how they are copied
       if (*(volatile int*)&sm.abort_flag) sm.ld_stop = i + 1;         // the warps leave together below
       if (lg < PT_ROWS) {
@@ -203,24 +237,21 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (stop != 0 && stop <= i + 1) break;
       const uint32_t v0 = sm.vmask[i & 3][0], v1 = sm.vmask[i & 3][1];
       const int rows = in_a ? box : PT_ROWS;          // rows per TMA box; box 0: pages that no box fits
-      bool in_time = true;
-      // each way: dims 0-255 as soon as the PV of the stage's last tile is past them, then the rest
+      // each way: dims 0-255 as soon as the PV of the slot's last tile is past them, then the rest
       if ((v0 & v1) == 0xffffffffu && (in_a ? !SPARSE && box > 0 : true)) {
-        // a run of rows, or of pages: the first thread of each box
-        if (lg < PT_ROWS && lg % rows == 0) {
-          const CUtensorMap* m = in_a ? &maps.pages : &maps.win;
+        // a run of rows, or of pages: a warp per atom, a lane per box (one thread takes 0.1 us a copy)
+        const CUtensorMap* m = in_a ? &maps.pages : &maps.win;
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
-            in_time = in_time && tc::mbar_wait(&sm.empty[st][x], ph);
-            if (!in_time) break;
-            if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[st][x], (at1 - at0) * ATOM);
-            for (int at = at0; at < at1; ++at)
-              tc::tma_load_2d(sm.kv[st][at] + lg * 128, m, &sm.full[st][x], 64 * at, y);
-            if (x) ++n_hi; else ++n_lo;
-          }
+        for (int x = 1; x >= 0; --x) {
+          const int at = (x ? PT_LO : 0) + (lg >> 5), at1 = x ? PT_ATOMS : PT_LO;
+          in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || half_free(x)));
+          if (!in_time) break;
+          if (lg == 0) tc::mbar_arrive_expect_tx(half_full(x), (x ? PT_ATOMS - PT_LO : PT_LO) * ATOM);
+          if (at < at1 && lane * rows < PT_ROWS)
+            tc::tma_load_2d(atom_of(at) + lane * rows * 128, m, half_full(x), 64 * at, sm.rowy[st][lane * rows]);
+          __syncwarp();
+          if (x) ++n_hi; else ++n_lo;
         }
-        __syncwarp();
       } else if ((v0 | v1) != 0u) {
         // scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp starts
         // 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the issue slots
@@ -229,11 +260,11 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         const int there = sm.rowy[st][v0 ? __ffs(v0) - 1 : 31 + __ffs(v1)];
         const CUtensorMap* m = in_a ? &maps.rows : &maps.win_rows;
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 1; x >= 0; --x) {
           const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
-          in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || tc::mbar_wait(&sm.empty[st][x], ph)));
+          in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || half_free(x)));
           if (!in_time) break;
-          if (lg == 0) tc::mbar_arrive_expect_tx(&sm.full[st][x], (at1 - at0) * ATOM);
+          if (lg == 0) tc::mbar_arrive_expect_tx(half_full(x), (at1 - at0) * ATOM);
           for (int p = lane * (PT_LDT / 32) + (lg >> 5); p < (at1 - at0) * (PT_ROWS / 4); p += PT_LDT) {
             const int quad = p & (PT_ROWS / 4 - 1), at = at0 + p / (PT_ROWS / 4);
             int4 r = *reinterpret_cast<const int4*>(&sm.rowy[st][4 * quad]);
@@ -241,24 +272,26 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
             r.y = r.y < 0 ? there : r.y;
             r.z = r.z < 0 ? there : r.z;
             r.w = r.w < 0 ? there : r.w;
-            tc::tma_gather4(sm.kv[st][at] + quad * 512, m, &sm.full[st][x], 64 * at, r);
+            tc::tma_gather4(atom_of(at) + quad * 512, m, half_full(x), 64 * at, r);
           }
           if (x) ++n_hi; else ++n_lo;
         }
       } else {
         // no row at all: zeros
-        in_time = __all_sync(0xffffffffu, lane != 0 || (tc::mbar_wait(&sm.empty[st][0], ph) && tc::mbar_wait(&sm.empty[st][1], ph)));
-        uint4* z = reinterpret_cast<uint4*>(sm.kv[st][0]);
-        for (int p = lg; p < PT_ATOMS * ATOM / 16 && in_time; p += PT_LDT) z[p] = make_uint4(0u, 0u, 0u, 0u);
+        in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || (half_free(0) && half_free(1))));
+        for (int p = lg; p < PT_ATOMS * ATOM / 16 && in_time; p += PT_LDT)
+          reinterpret_cast<uint4*>(atom_of(p / (ATOM / 16)))[p % (ATOM / 16)] = make_uint4(0u, 0u, 0u, 0u);
         tc::fence_proxy_async_smem();
         named_bar(1, PT_LDT);
         if (lg == 0) {
-          tc::mbar_arrive(&sm.full[st][0]);
-          tc::mbar_arrive(&sm.full[st][1]);
+          tc::mbar_arrive(half_full(0));
+          tc::mbar_arrive(half_full(1));
         }
         ++n_lo;
         ++n_hi;
       }
+      lo.step(2);
+      hi.step(3);
       if (!in_time) atomicExch(&sm.abort_flag, 1);
       now = next;
       next = page_of(after);
@@ -266,9 +299,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     }
     // drain: no TMA write of this CTA may be in flight when the CTA exits
     if (lg == 0)
-      for (int q = 0; q < 4; ++q) {
-        const int uses = ((q & 1 ? n_hi : n_lo) + 1 - (q >> 1)) >> 1;     // of stage q / 2
-        if (uses > 0) tc::mbar_wait(&sm.full[q >> 1][q & 1], (uses - 1) & 1);
+      for (int q = 0; q < 5; ++q) {
+        const int uses = q < 2 ? (n_lo + 1 - q) / 2 : (n_hi + 4 - q) / 3;      // of a ring's slot
+        if (uses > 0) tc::mbar_wait(q < 2 ? &sm.lo_full[q] : &sm.hi_full[q - 2], (uses - 1) & 1);
       }
     __syncwarp();
   } else if (warp == PT_SW) {
@@ -279,7 +312,8 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     // traffic each test of a barrier takes hundreds.)
     constexpr uint32_t ID_S = tc::idesc(tc::FMT_BF16, tc::FMT_BF16, PT_HC, PT_ROWS);
     const uint64_t q_d = tc::desc_k_sw128(tc::smem_u32(sm.q[0]));
-    const uint64_t k_d0 = tc::desc_k_sw128(tc::smem_u32(sm.kv[0][0])), k_d1 = tc::desc_k_sw128(tc::smem_u32(sm.kv[1][0]));
+    const uint64_t lo_d = tc::desc_k_sw128(tc::smem_u32(sm.lo[0][0])), hi_d = tc::desc_k_sw128(tc::smem_u32(sm.hi[0][0]));
+    RingPos lo{0, 0}, hi{0, 0};
     if (lane == 0) {
       tc::prefetch_tmap(&maps.q);
       tc::prefetch_tmap(&maps.pages);
@@ -292,9 +326,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       // the segment before no longer reads Q once its last S is complete
       if (n > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.qfree, (n - 1) & 1))) { ok = false; break; }
       if (tc::elect_one()) {
-        tc::mbar_arrive_expect_tx(&sm.qfull, PT_ATOMS * PT_HC * 128);
-        for (int at = 0; at < PT_ATOMS; ++at)
-          tc::tma_load_2d(sm.q[at], &maps.q, &sm.qfull, 64 * at, seg.b * a.H + hh * PT_HC);
+        tc::mbar_arrive_expect_tx(&sm.qfull, (PT_ATOMS - PT_QT) * PT_HC * 128);
+        for (int at = PT_QT; at < PT_ATOMS; ++at)
+          tc::tma_load_2d(sm.q[at - PT_QT], &maps.q, &sm.qfull, 64 * at, seg.b * a.H + hh * PT_HC);
       }
       __syncwarp();
       for (int64_t t = seg.t0; t < seg.t1; ++i) {
@@ -302,24 +336,52 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         // instructions in; cold, the first S took 4 us, later ones 1.
         const uint32_t live = i > 0;
         const int x = i - 1, st = x & 1;
-        const uint32_t ph = (x >> 1) & 1, d = tmem + TM_S + st * 32;
-        const uint64_t kd = st ? k_d1 : k_d0;
-        // (the tile's S buffer is free: its stage was refilled after the PV that used it)
-        bool go = !live || ((t > seg.t0 || tc::mbar_wait(&sm.qfull, n & 1)) && tc::mbar_wait(&sm.full[st][0], ph));
+        const uint32_t d = tmem + TM_S + st * 32;
+        if (live && t == seg.t0) {
+          // the queries to TMEM (their slots are free again once that is done), and the rest of them
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.lo_full[lo.at], lo.ph));
+          if (ok && tc::elect_one()) {
+#pragma unroll 1
+            for (int at = 0; at < PT_LO; ++at)
+              tc::cp_atom_ws(tmem + TM_Q + 32 * at, lo_d + (uint64_t)((lo.at * PT_LO + at) * (ATOM >> 4)));
+            tc::mma_commit(&sm.lo_empty[lo.at]);
+          }
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.hi_full[hi.at], hi.ph));
+          if (ok && tc::elect_one()) {
+#pragma unroll 1
+            for (int at = PT_LO; at < PT_QT; ++at)
+              tc::cp_atom_ws(tmem + TM_Q + 32 * at, hi_d + (uint64_t)((hi.at * (PT_ATOMS - PT_LO) + at - PT_LO) * (ATOM >> 4)));
+            tc::mma_commit(&sm.hi_empty[hi.at]);
+          }
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(&sm.qfull, n & 1));
+          if (!ok) break;
+          lo.step(2);
+          hi.step(3);
+        }
+        const uint64_t kl = lo_d + (uint64_t)(lo.at * PT_LO * (ATOM >> 4)), kh = hi_d + (uint64_t)(hi.at * (PT_ATOMS - PT_LO) * (ATOM >> 4));
+        // (S of two tiles before has been read)
+        const bool go = !live || (tc::mbar_wait(&sm.sfree[st], ((x >> 1) & 1) ^ 1) && tc::mbar_wait(&sm.hi_full[hi.at], hi.ph));
         ok = __all_sync(0xffffffffu, go && !*(volatile int*)&sm.abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int at = 0; at < PT_LO; ++at)            // 4 steps of 16 dims an atom; atoms are 8 KB apart
-          tc::mma_f16_ws_x4<2>(d, q_d + (uint64_t)(at * (ATOM >> 4)), kd + (uint64_t)(at * (ATOM >> 4)), ID_S, at > 0, live);
-        ok = __all_sync(0xffffffffu, !live || tc::mbar_wait(&sm.full[st][1], ph));
+        for (int at = PT_LO; at < PT_QT; ++at)        // 4 steps of 16 dims an atom; atoms are 8 KB apart
+          tc::mma_f16_ws_ts_x4<2>(d, tmem + TM_Q + 32 * at, kh + (uint64_t)((at - PT_LO) * (ATOM >> 4)), ID_S, at > PT_LO, live);
+#pragma unroll
+        for (int at = PT_QT; at < PT_ATOMS; ++at)
+          tc::mma_f16_ws_x4<2>(d, q_d + (uint64_t)((at - PT_QT) * (ATOM >> 4)), kh + (uint64_t)((at - PT_LO) * (ATOM >> 4)), ID_S, 1, live);
+        ok = __all_sync(0xffffffffu, !live || tc::mbar_wait(&sm.lo_full[lo.at], lo.ph));
         if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int at = PT_LO; at < PT_ATOMS; ++at)
-          tc::mma_f16_ws_x4<2>(d, q_d + (uint64_t)(at * (ATOM >> 4)), kd + (uint64_t)(at * (ATOM >> 4)), ID_S, 1, live);
+        for (int at = 0; at < PT_LO; ++at)
+          tc::mma_f16_ws_ts_x4<2>(d, tmem + TM_Q + 32 * at, kl + (uint64_t)(at * (ATOM >> 4)), ID_S, 1, live);
         if (live) {
           ++t;
+          lo.step(2);
+          hi.step(3);
           if (tc::elect_one()) {
             tc::mma_commit(&sm.sfull[st]);
             if (t == seg.t1) tc::mma_commit(&sm.qfree);
@@ -341,35 +403,40 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     // rows of 128 bytes).
     constexpr uint32_t ID_O = tc::idesc(tc::FMT_BF16, tc::FMT_BF16, PT_HC, 256, 0, 1);
     const uint64_t p_d = tc::desc_k_sw128(tc::smem_u32(sm.p));
-    const uint64_t pl_d0 = tc::desc_k_sw128(tc::smem_u32(sm.kv[0][PT_ATOMS - 1])),
-                   pl_d1 = tc::desc_k_sw128(tc::smem_u32(sm.kv[1][PT_ATOMS - 1]));
-    const uint64_t v_d0 = tc::desc_mn_sw128(tc::smem_u32(sm.kv[0][0]), ATOM, 1024),
-                   v_d1 = tc::desc_mn_sw128(tc::smem_u32(sm.kv[1][0]), ATOM, 1024);
+    const uint64_t pl_d0 = tc::desc_k_sw128(tc::smem_u32(sm.hi[0][PT_ATOMS - PT_LO - 1]));
+    const uint64_t lo_d = tc::desc_mn_sw128(tc::smem_u32(sm.lo[0][0]), ATOM, 1024), hi_d = tc::desc_mn_sw128(tc::smem_u32(sm.hi[0][0]), ATOM, 1024);
+    RingPos lo{0, 0}, hi{0, 0};
     bool ok = true;
     int n = 0, i = 0;
     for (; ok && seg.next(a); ++n) {
       for (int64_t t = seg.t0; t < seg.t1; ++i) {
         const uint32_t live = i > 0;                  // the first turn issues nothing, as above
-        const int x = i - 1, st = x & 1;
-        const uint64_t vd = st ? v_d1 : v_d0, pl = st ? pl_d1 : pl_d0;
+        const int x = i - 1;
         const bool first = t == seg.t0;               // overwrites O, which the epilogue before has read
+        if (live && first) {                          // past the queries' slots
+          lo.step(2);
+          hi.step(3);
+        }
+        const uint64_t hi_at = (uint64_t)(hi.at * (PT_ATOMS - PT_LO) * (ATOM >> 4));
+        const uint64_t vd = lo_d + (uint64_t)(lo.at * PT_LO * (ATOM >> 4)), vh = hi_d + hi_at, pl = pl_d0 + hi_at;
         const bool go = !live || ((!first || n == 0 || tc::mbar_wait(&sm.ofree, (n - 1) & 1)) && tc::mbar_wait(&sm.pfull, x & 1));
         ok = __all_sync(0xffffffffu, go && !*(volatile int*)&sm.abort_flag);
         if (!ok) break;
         tc::fence_after_sync();
         tc::mma_f16_ws_x4<128>(tmem + TM_O, p_d, vd, ID_O, !first, live);
         tc::mma_f16_ws_x4<128>(tmem + TM_O, pl, vd, ID_O, 1, live);
-        if (live && tc::elect_one()) tc::mma_commit(&sm.empty[st][0]);
+        if (live && tc::elect_one()) tc::mma_commit(&sm.lo_empty[lo.at]);
         __syncwarp();
-        const uint64_t vh = vd + (uint64_t)(PT_LO * (ATOM >> 4));
         tc::mma_f16_ws_x4<128>(tmem + TM_O + 128, p_d, vh, ID_O, !first, live);
         tc::mma_f16_ws_x4<128>(tmem + TM_O + 128, pl, vh, ID_O, 1, live);
         if (live) {
           ++t;
           if (tc::elect_one()) {
-            tc::mma_commit(&sm.empty[st][1]);
+            tc::mma_commit(&sm.hi_empty[hi.at]);
             tc::mma_commit(&sm.pdone);
           }
+          lo.step(2);
+          hi.step(3);
         }
         __syncwarp();
       }
@@ -402,6 +469,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     const float scale = fmaxf(fabsf(scale2), 1.2e-38f);          // not 0: an absent row's -inf must stay one
     bool ok = true;
     int i = 0;                                        // tiles so far, over all segments
+    RingPos lo{0, 0}, hi{0, 0};
     // sequences without a row (no unit has a tile of theirs): a lane looks at each, the warp clears
     for (int b0 = unit + warp * 32 * a.units; b0 < a.B; b0 += PT_SMW * 32 * a.units) {
       const int64_t bl = (int64_t)b0 + (int64_t)lane * a.units;
@@ -419,10 +487,12 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     while (ok && seg.next(a)) {
       const float sink = hv ? a.sink[h] : 0.f;
       float m_run = -INFINITY, l_run = 0.f;           // running maximum; this thread's row sum
-      for (int64_t t = seg.t0; t < seg.t1; ++t, ++i) {
+      lo.step(2);                                     // past the queries' slots
+      hi.step(3);
+      for (int64_t t = seg.t0; t < seg.t1; ++t, ++i, lo.step(2), hi.step(3)) {
         const int st = i & 1;
         const uint32_t ph = (i >> 1) & 1;
-        bool w = tc::mbar_wait(&sm.full[st][0], ph);  // the mask of the tile's rows
+        bool w = tc::mbar_wait(&sm.lo_full[lo.at], lo.ph);      // the mask of the tile's rows
         const uint32_t vm = sm.vmask[i & 3][half] >> (16 * wg);
         w = w && tc::mbar_wait(&sm.sfull[st], ph);
         w = __all_sync(0xffffffffu, w && !*(volatile int*)&sm.abort_flag);
@@ -437,6 +507,8 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
           for (int j = 0; j < 16; ++j) s[j] = __uint_as_float(v[j]);
         }
         tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.sfree[st]);
         if (scale2 < 0.f) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] = -s[j];
@@ -505,7 +577,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         }
         {
           // P_lo goes to the stage's rotary atom: S of this tile, its only reader, is complete
-          const uint32_t pbase = tc::smem_u32(sm.p), lbase = tc::smem_u32(sm.kv[st][PT_ATOMS - 1]);
+          const uint32_t pbase = tc::smem_u32(sm.p), lbase = tc::smem_u32(sm.hi[hi.at][PT_ATOMS - PT_LO - 1]);
           const int c0 = 4 * half + 2 * wg;           // 16-byte chunks (8 rows) of the head's P
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {

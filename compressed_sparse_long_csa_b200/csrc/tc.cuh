@@ -167,6 +167,34 @@ __device__ __forceinline__ void mma_f16_ws_x4(uint32_t d_tmem, uint64_t a_desc, 
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc), "r"(live), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
       : "memory");
 }
+// The same with A in tensor memory: K-step k at columns a_tmem + 8 k, row r in lanes r and r + 64.
+template <int BSTEP>
+__device__ __forceinline__ void mma_f16_ws_ts_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t acc, uint32_t live) {
+  asm volatile(
+      "{\n\t.reg .pred e, l, p, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 l, %5, 0;\n\t"
+      "and.pred e, e, l;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, %6;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, %7;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, %8;\n\t"
+      "@e tcgen05.mma.ws.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc), "r"(live), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
+      : "memory");
+}
+// A 64-row swizzle atom (128 bytes a row) from shared memory to 32 columns of tensor memory, as such
+// an A: row r to lanes r and r + 64.  One thread; in order before the MMAs that it issues afterwards.
+__device__ __forceinline__ void cp_atom_ws(uint32_t d_tmem, uint64_t desc) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)                         // 16 bytes of each row, 4 columns
+    asm volatile("tcgen05.cp.cta_group::1.64x128b.warpx2::02_13 [%0], %1;" ::"r"(d_tmem + 4 * c), "l"(desc + c) : "memory");
+}
 // One lane of a converged warp (the same lane every time the whole warp calls it).  MMAs
 // are issued as `if (elect_one()) mma(...)` by a converged warp whose lanes all compute the
 // (warp-uniform) descriptors: the issue then keeps pace with N = 64 MMAs, where a lone
