@@ -205,17 +205,17 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     auto half_free = [&](int x) { return x ? tc::mbar_wait(&sm.hi_empty[hi.at], hi.ph ^ 1) : tc::mbar_wait(&sm.lo_empty[lo.at], lo.ph ^ 1); };
     auto half_full = [&](int x) { return x ? &sm.hi_full[hi.at] : &sm.lo_full[lo.at]; };
     auto atom_of = [&](int at) { return at < PT_LO ? sm.lo[lo.at][at] : sm.hi[hi.at][at - PT_LO]; };
-    static_assert(PT_QT == PT_LDT / 32 && PT_ATOMS - PT_LO <= PT_LDT / 32, "an atom a warp");
+    static_assert(PT_LO == 4 && PT_QT == 6 && PT_LDT == 192, "a warp's atoms");
     for (int i = 0; now.is; ++i) {
       bool in_time = true;
       if (now.first) {
-        // a segment's first slots bring the queries' atoms for TMEM, an atom a warp
-        const int at = lg >> 5;
-        if (lane == 0) {
-          in_time = half_free(at >= PT_LO);
-          if (at == 0) tc::mbar_arrive_expect_tx(half_full(0), PT_LO * ATOM);
-          if (at == PT_LO) tc::mbar_arrive_expect_tx(half_full(1), (PT_QT - PT_LO) * ATOM);
-          if (in_time) tc::tma_load_2d(atom_of(at), &maps.q, half_full(at >= PT_LO), 64 * at, now.b * a.H + hh * PT_HC);
+        // a segment's first slots bring the queries' atoms for TMEM, by the four warps that look up no rows
+        const int w = (lg >> 5) - 2, x = w >> 1;      // warps 2 and 3: two atoms of dims 0-255 each; 4 and 5: one of the rest
+        if (w >= 0 && lane == 0) {
+          in_time = half_free(x);
+          if ((w & 1) == 0) tc::mbar_arrive_expect_tx(half_full(x), (x ? PT_QT - PT_LO : PT_LO) * ATOM);
+          for (int at = x ? PT_LO + (w & 1) : 2 * w; in_time && at < (x ? PT_LO + 1 + (w & 1) : 2 * w + 2); ++at)
+            tc::tma_load_2d(atom_of(at), &maps.q, half_full(x), 64 * at, now.b * a.H + hh * PT_HC);
         }
         in_time = __shfl_sync(0xffffffffu, in_time, 0);
         ++n_lo;
