@@ -754,6 +754,7 @@ static csa_status run_paged_attention(PagedAttnArgs& a, int dtype, void* workspa
   REQUIRE(workspace && ws_bytes >= attn_decode_paged_workspace_size(a.B, a.H, a.dv, paged_rows_max(a)), CSA_ERR_WORKSPACE);
   REQUIRE(aligned16(workspace), CSA_ERR_ALIGN);
   a.part = (float*)workspace;
+  paged_divisor(a);
   a.err = device_error_word();
   REQUIRE(a.err, CSA_ERR_CUDA);
   if (tc_enabled() && dtype == CSA_BF16 && a.dk == 576 && a.dv == 512) return cuda_status(launch_paged_attn_tc(a, S(stream)));

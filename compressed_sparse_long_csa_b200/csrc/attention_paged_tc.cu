@@ -167,13 +167,14 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     const int lg = threadIdx.x - PT_LDW * 32;
     struct Row {
       bool is, in_a, first;                           // a tile of the unit; of the entries (else of the window); of its segment
-      int b, e, id;                                   // sequence; entry (or the window's row), -1 = none; page id
+      int b, e, at, id;                               // sequence; entry (or the window's row), -1 = none; its row in the page; page id
     };
+    const int cap = (int)paged_capacity(a);
     int64_t t = 0;
     bool more = seg.next(a);
     if (more) t = seg.t0;
     auto entry_of = [&]() {                           // the next tile: the entry
-      Row r{more, t < seg.ta, t == seg.t0, seg.b, -1, 0};
+      Row r{more, t < seg.ta, t == seg.t0, seg.b, -1, 0, 0};
       if (!more) return r;
       if (lg < PT_ROWS) {
         const int64_t v = (r.in_a ? t : t - seg.ta) * PT_ROWS + lg;
@@ -187,15 +188,18 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       return r;
     };
     auto page_of = [&](Row r) {                       // its page
-      if (r.in_a && r.e >= 0 && (!SPARSE || r.e < paged_capacity(a)))
-        r.id = a.table[(size_t)r.b * a.table_w + (unsigned)r.e / (unsigned)a.page];
-      else r.id = -1;
+      r.id = -1;
+      if (r.in_a && r.e >= 0 && (!SPARSE || r.e < cap)) {
+        const int pg = paged_page(a, r.e);
+        r.at = r.e - pg * a.page;
+        r.id = a.table[(size_t)r.b * a.table_w + pg];
+      }
       return r;
     };
     auto row_of = [&](const Row& r) {                 // its row of the pool or the window, -1 = none
       if (!r.in_a || r.e < 0) return r.e;
-      if (r.id < 0 || r.id >= a.n_pages) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
-      return (int)((int64_t)r.id * a.page + (unsigned)r.e % (unsigned)a.page);
+      if ((unsigned)r.id >= (unsigned)a.n_pages) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
+      return r.id * a.page + r.at;                    // (a pool has less than 2^31 rows)
     };
     Row now = entry_of(), next = entry_of(), after = entry_of();
     now = page_of(now);

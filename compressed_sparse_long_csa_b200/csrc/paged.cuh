@@ -27,6 +27,8 @@ struct PagedAttnArgs {
   const void* pages;          // [n_pages, page, dk]
   int64_t n_pages;
   int page;
+  unsigned page_mul;          // e / page = e * page_mul >> page_shift for 0 <= e < 2^31 (paged_divisor)
+  int page_shift;
   const int32_t* table;       // [B, table_w] page of each run of `page` entries
   int table_w;
   const int32_t* n_entries;   // [B] (dense) or null
@@ -47,6 +49,19 @@ struct PagedAttnArgs {
   int begin_cost;             // what beginning a sequence costs a unit, in tiles
   unsigned* err;
 };
+
+// Sets the multiplier: 2^(31 + s) / page rounded up, 2^s the power of two from page up.  It is off by
+// less than 1, so e times it by less than 2^31 <= 2^(31 + s) / page: the quotient is exact.
+inline void paged_divisor(PagedAttnArgs& a) {
+  int s = 0;
+  while ((1 << s) < a.page) ++s;
+  a.page_mul = (unsigned)(((1ull << (31 + s)) + a.page - 1) / a.page);
+  a.page_shift = 31 + s;
+}
+// The page that holds entry e (a division costs a dependent chain of some 30 instructions).
+__device__ __forceinline__ int paged_page(const PagedAttnArgs& a, int e) {
+  return (int)((unsigned long long)(unsigned)e * a.page_mul >> a.page_shift);
+}
 
 // Entries that the table has room for.
 __host__ __device__ inline int64_t paged_capacity(const PagedAttnArgs& a) { return (int64_t)a.table_w * a.page; }
@@ -221,10 +236,9 @@ __device__ __forceinline__ int64_t paged_row(const PagedAttnArgs& a, int b, int 
     if (e < 0) return -1;
     if ((int64_t)e >= paged_capacity(a)) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
   }
-  const unsigned pg = (unsigned)e / (unsigned)a.page;
-  const int id = a.table[(size_t)b * a.table_w + pg];
+  const int pg = paged_page(a, e), id = a.table[(size_t)b * a.table_w + pg];
   if (id < 0 || (int64_t)id >= a.n_pages) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
-  return (int64_t)id * a.page + (e - (int)pg * a.page);
+  return (int64_t)id * a.page + (e - pg * a.page);
 }
 
 // Units of an attention launch over `ctas` CTAs per head group: no more than the tiles that
