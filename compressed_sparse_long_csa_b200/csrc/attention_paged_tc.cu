@@ -41,12 +41,13 @@ constexpr int PT_ROWS = 64;              // rows per tile (N of QK^T, K of PV)
 constexpr int PT_HC = 64;                // heads per CTA (MMA M)
 constexpr int PT_ATOMS = 9;              // 576 dims = 9 atoms of 64 dims (128 bytes)
 constexpr int PT_LO = 4;                 // atoms of a tile's first half (dims 0-255)
-constexpr int PT_LDT = 192;              // loader threads
 constexpr int PT_SMW = 8;                // softmax warps: two warpgroups, one per half of a lane's columns
 constexpr int PT_SW = 8;                 // the warp of the queries and S
 constexpr int PT_PVW = 9;                // the warp of PV
-constexpr int PT_LDW = 10;               // first loader warp
-constexpr int PT_THREADS = PT_LDW * 32 + PT_LDT;
+constexpr int PT_LDW = 10;               // the warp that looks rows up
+constexpr int PT_CPW = 11;               // first of five that copy them
+constexpr int PT_CPT = 160, PT_LDT = 32 + PT_CPT;           // threads of the latter; of both
+constexpr int PT_THREADS = PT_CPW * 32 + PT_CPT;
 constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 12.6 us in one unit, 14.5 in two and a merge)
 constexpr int PT_BEGIN_COST = 2;         // (1: ragged batch 109.0 us, 2: 106.7, 3: 108.5)
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
@@ -159,67 +160,28 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
   PagedSeg seg;                                     // every role walks the unit's segments by itself
   seg.start(plan, unit);
 
-  if (warp >= PT_LDW) {
-    // ------------------------------------------------------------------ loader (6 warps)
-    // Tile i of the unit, counted over all segments, goes to stage i % 2.  Thread j < 64 looks up row
-    // j of the tiles ahead, a step of the chain entry -> page -> row per tile, so that no load is
-    // waited for where it is issued.
-    const int lg = threadIdx.x - PT_LDW * 32;
-    struct Row {
-      bool is, in_a, first;                           // a tile of the unit; of the entries (else of the window); of its segment
-      int b, e, at, id;                               // sequence; entry (or the window's row), -1 = none; its row in the page; page id
-    };
-    const int cap = (int)paged_capacity(a);
-    int64_t t = 0;
-    bool more = seg.next(a);
-    if (more) t = seg.t0;
-    auto entry_of = [&]() {                           // the next tile: the entry
-      Row r{more, t < seg.ta, t == seg.t0, seg.b, -1, 0, 0};
-      if (!more) return r;
-      if (lg < PT_ROWS) {
-        const int64_t v = (r.in_a ? t : t - seg.ta) * PT_ROWS + lg;
-        if (!r.in_a) r.e = v < seg.nw ? seg.b * a.W + (int)v : -1;
-        else if (v < seg.na) r.e = SPARSE ? a.idx[(size_t)seg.b * a.k + v] : (int)v;
-      }
-      if (++t == seg.t1) {
-        more = seg.next(a);
-        t = seg.t0;
-      }
-      return r;
-    };
-    auto page_of = [&](Row r) {                       // its page
-      r.id = -1;
-      if (r.in_a && r.e >= 0 && (!SPARSE || r.e < cap)) {
-        const int pg = paged_page(a, r.e);
-        r.at = r.e - pg * a.page;
-        r.id = a.table[(size_t)r.b * a.table_w + pg];
-      }
-      return r;
-    };
-    auto row_of = [&](const Row& r) {                 // its row of the pool or the window, -1 = none
-      if (!r.in_a || r.e < 0) return r.e;
-      if ((unsigned)r.id >= (unsigned)a.n_pages) { raise_err(a.err, CSA_DEVERR_INDEX); return -1; }
-      return r.id * a.page + r.at;                    // (a pool has less than 2^31 rows)
-    };
-    Row now = entry_of(), next = entry_of(), after = entry_of();
-    now = page_of(now);
-    next = page_of(next);
+  if (warp >= PT_CPW) {
+    // ------------------------------------------------------------------ copies (5 warps)
+    // Ring slots, in order: per segment one for the queries' atoms that go to TMEM, then its tiles.
+    const int w = warp - PT_CPW, ct = threadIdx.x - PT_CPW * 32;
     RingPos lo{0, 0}, hi{0, 0};                       // the next slot of each ring
     int n_lo = 0, n_hi = 0;                           // slots started (for the drain)
     auto half_free = [&](int x) { return x ? tc::mbar_wait(&sm.hi_empty[hi.at], hi.ph ^ 1) : tc::mbar_wait(&sm.lo_empty[lo.at], lo.ph ^ 1); };
     auto half_full = [&](int x) { return x ? &sm.hi_full[hi.at] : &sm.lo_full[lo.at]; };
     auto atom_of = [&](int at) { return at < PT_LO ? sm.lo[lo.at][at] : sm.hi[hi.at][at - PT_LO]; };
-    static_assert(PT_LO == 4 && PT_QT == 6 && PT_LDT == 192, "a warp's atoms");
-    for (int i = 0; now.is; ++i) {
+    int i = 0;
+    bool go_on = true;
+    while (go_on && seg.next(a)) {
       bool in_time = true;
-      if (now.first) {
-        // a segment's first slots bring the queries' atoms for TMEM, by the four warps that look up no rows
-        const int w = (lg >> 5) - 2, x = w >> 1;      // warps 2 and 3: two atoms of dims 0-255 each; 4 and 5: one of the rest
-        if (w >= 0 && lane == 0) {
+      {
+        // warps 0-3: an atom of dims 0-255 each; 4: the next two
+        static_assert(PT_LO == 4 && PT_QT == 6 && PT_CPT == 160, "a warp's atoms");
+        const int x = w >> 2;
+        if (lane == 0) {
           in_time = half_free(x);
-          if ((w & 1) == 0) tc::mbar_arrive_expect_tx(half_full(x), (x ? PT_QT - PT_LO : PT_LO) * ATOM);
-          for (int at = x ? PT_LO + (w & 1) : 2 * w; in_time && at < (x ? PT_LO + 1 + (w & 1) : 2 * w + 2); ++at)
-            tc::tma_load_2d(atom_of(at), &maps.q, half_full(x), 64 * at, now.b * a.H + hh * PT_HC);
+          if ((w & 3) == 0) tc::mbar_arrive_expect_tx(half_full(x), (x ? PT_QT - PT_LO : PT_LO) * ATOM);
+          for (int at = w; in_time && at < w + 1 + x; ++at)
+            tc::tma_load_2d(atom_of(at), &maps.q, half_full(x), 64 * at, seg.b * a.H + hh * PT_HC);
         }
         in_time = __shfl_sync(0xffffffffu, in_time, 0);
         ++n_lo;
@@ -227,87 +189,141 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         lo.step(2);
         hi.step(3);
       }
-      const int st = i & 1, y = row_of(now);
-      const bool in_a = now.in_a;
-      // what needs no free stage comes first: the rows, which of them exist, how they are copied
-      if (*(volatile int*)&sm.abort_flag) sm.ld_stop = i + 1;         // the warps leave together below
-      if (lg < PT_ROWS) {
-        sm.rowy[st][lg] = y;                          // (every warp is past the copies of two tiles before)
-        const uint32_t vb = __ballot_sync(0xffffffffu, y >= 0);
-        if ((lg & 31) == 0) sm.vmask[i & 3][lg >> 5] = vb;
-      }
-      named_bar(1, PT_LDT);
-      const int stop = *(volatile int*)&sm.ld_stop;
-      if (stop != 0 && stop <= i + 1) break;
-      const uint32_t v0 = sm.vmask[i & 3][0], v1 = sm.vmask[i & 3][1];
-      const int rows = in_a ? box : PT_ROWS;          // rows per TMA box; box 0: pages that no box fits
-      // each way: dims 0-255 as soon as the PV of the slot's last tile is past them, then the rest
-      if ((v0 & v1) == 0xffffffffu && (in_a ? !SPARSE && box > 0 : true)) {
-        // a run of rows, or of pages: a warp per atom, a lane per box (one thread takes 0.1 us a copy)
-        const CUtensorMap* m = in_a ? &maps.pages : &maps.win;
-#pragma unroll 1
-        for (int x = 1; x >= 0; --x) {
-          const int at = (x ? PT_LO : 0) + (lg >> 5), at1 = x ? PT_ATOMS : PT_LO;
-          in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || half_free(x)));
-          if (!in_time) break;
-          if (lg == 0) tc::mbar_arrive_expect_tx(half_full(x), (x ? PT_ATOMS - PT_LO : PT_LO) * ATOM);
-          if (at < at1 && lane * rows < PT_ROWS)
-            tc::tma_load_2d(atom_of(at) + lane * rows * 128, m, half_full(x), 64 * at, sm.rowy[st][lane * rows]);
-          __syncwarp();
-          if (x) ++n_hi; else ++n_lo;
-        }
-      } else if ((v0 | v1) != 0u) {
-        // scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp starts
-        // 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the issue slots
-        // and shared-memory ports that the softmax uses).  An absent row is a second copy of one
-        // that is there: its P is 0, and what it holds must not be less finite than the rest.
-        const int there = sm.rowy[st][v0 ? __ffs(v0) - 1 : 31 + __ffs(v1)];
-        const CUtensorMap* m = in_a ? &maps.rows : &maps.win_rows;
+      for (int64_t t = seg.t0; t < seg.t1; ++t, ++i) {
+        const int st = i & 1;
+        const bool in_a = t < seg.ta;
+        if (*(volatile int*)&sm.abort_flag || !in_time) sm.ld_stop = i + 1;       // all leave together below
+        named_bar(1, PT_LDT);                         // the tile's rows are there
+        const int stop = *(volatile int*)&sm.ld_stop;
+        if (stop != 0 && stop <= i + 1) { go_on = false; break; }
+        const uint32_t v0 = sm.vmask[i & 3][0], v1 = sm.vmask[i & 3][1];
+        const int rows = in_a ? box : PT_ROWS;        // rows per TMA box; box 0: pages that no box fits
+        const bool boxes = (v0 & v1) == 0xffffffffu && (in_a ? !SPARSE && box > 0 : true);
+        // Dims 256-575 (x = 1) first, whose slot has long been free; dims 0-255 as soon as the PV of two
+        // tiles before is past them.
 #pragma unroll 1
         for (int x = 1; x >= 0; --x) {
           const int at0 = x ? PT_LO : 0, at1 = x ? PT_ATOMS : PT_LO;
-          in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || half_free(x)));
-          if (!in_time) break;
-          if (lg == 0) tc::mbar_arrive_expect_tx(half_full(x), (at1 - at0) * ATOM);
-          for (int p = lane * (PT_LDT / 32) + (lg >> 5); p < (at1 - at0) * (PT_ROWS / 4); p += PT_LDT) {
-            const int quad = p & (PT_ROWS / 4 - 1), at = at0 + p / (PT_ROWS / 4);
-            int4 r = *reinterpret_cast<const int4*>(&sm.rowy[st][4 * quad]);
-            r.x = r.x < 0 ? there : r.x;
-            r.y = r.y < 0 ? there : r.y;
-            r.z = r.z < 0 ? there : r.z;
-            r.w = r.w < 0 ? there : r.w;
-            tc::tma_gather4(atom_of(at) + quad * 512, m, half_full(x), 64 * at, r);
+          // (one thread polls: five warps that do slow the MMAs' operands)
+          if (ct == 0 && !half_free(x)) atomicExch(&sm.abort_flag, 1);
+          named_bar(2, PT_CPT);
+          in_time = !*(volatile int*)&sm.abort_flag;
+          if ((v0 | v1) == 0u) {
+            // no row at all: zeros
+            for (int p = ct; p < (at1 - at0) * ATOM / 16 && in_time; p += PT_CPT)
+              reinterpret_cast<uint4*>(atom_of(at0))[p] = make_uint4(0u, 0u, 0u, 0u);
+            tc::fence_proxy_async_smem();
+            named_bar(2, PT_CPT);
+            if (ct == 0) tc::mbar_arrive(half_full(x));
+          } else if (in_time) {
+            if (ct == 0) tc::mbar_arrive_expect_tx(half_full(x), (at1 - at0) * ATOM);
+            if (boxes) {
+              // a run of rows, or of pages: atoms over the warps, a lane per box (one thread takes 0.1 us a copy)
+              for (int at = at0 + w; at < at1; at += PT_CPT / 32)
+                if (lane * rows < PT_ROWS)
+                  tc::tma_load_2d(atom_of(at) + lane * rows * 128, in_a ? &maps.pages : &maps.win, half_full(x), 64 * at, sm.rowy[st][lane * rows]);
+            } else {
+              // scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp starts
+              // 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the issue slots
+              // and shared-memory ports that the softmax uses).  An absent row is a second copy of one
+              // that is there: its P is 0, and what it holds must not be less finite than the rest.
+              const int there = sm.rowy[st][v0 ? __ffs(v0) - 1 : 31 + __ffs(v1)];
+              const CUtensorMap* m = in_a ? &maps.rows : &maps.win_rows;
+              for (int p = lane * (PT_CPT / 32) + w; p < (at1 - at0) * (PT_ROWS / 4); p += PT_CPT) {
+                const int quad = p & (PT_ROWS / 4 - 1), at = at0 + p / (PT_ROWS / 4);
+                int4 r = *reinterpret_cast<const int4*>(&sm.rowy[st][4 * quad]);
+                r.x = r.x < 0 ? there : r.x;
+                r.y = r.y < 0 ? there : r.y;
+                r.z = r.z < 0 ? there : r.z;
+                r.w = r.w < 0 ? there : r.w;
+                tc::tma_gather4(atom_of(at) + quad * 512, m, half_full(x), 64 * at, r);
+              }
+            }
+            __syncwarp();
+            if (x) ++n_hi; else ++n_lo;
           }
-          if (x) ++n_hi; else ++n_lo;
         }
-      } else {
-        // no row at all: zeros
-        in_time = __all_sync(0xffffffffu, in_time && (lane != 0 || (half_free(0) && half_free(1))));
-        for (int p = lg; p < PT_ATOMS * ATOM / 16 && in_time; p += PT_LDT)
-          reinterpret_cast<uint4*>(atom_of(p / (ATOM / 16)))[p % (ATOM / 16)] = make_uint4(0u, 0u, 0u, 0u);
-        tc::fence_proxy_async_smem();
-        named_bar(1, PT_LDT);
-        if (lg == 0) {
-          tc::mbar_arrive(half_full(0));
-          tc::mbar_arrive(half_full(1));
-        }
-        ++n_lo;
-        ++n_hi;
+        lo.step(2);
+        hi.step(3);
+        if (!in_time) atomicExch(&sm.abort_flag, 1);
       }
-      lo.step(2);
-      hi.step(3);
-      if (!in_time) atomicExch(&sm.abort_flag, 1);
-      now = next;
-      next = page_of(after);
-      after = entry_of();
     }
     // drain: no TMA write of this CTA may be in flight when the CTA exits
-    if (lg == 0)
+    if (ct == 0)
       for (int q = 0; q < 5; ++q) {
         const int uses = q < 2 ? (n_lo + 1 - q) / 2 : (n_hi + 4 - q) / 3;      // of a ring's slot
         if (uses > 0) tc::mbar_wait(q < 2 ? &sm.lo_full[q] : &sm.hi_full[q - 2], (uses - 1) & 1);
       }
     __syncwarp();
+  } else if (warp >= PT_LDW) {
+    // ------------------------------------------------------------------ row lookups
+    // Lane j looks up rows j and j + 32 of the tiles ahead, a step of the chain entry -> page -> row per
+    // tile, so that no load is waited for where it is issued; the rows of tile i + 1 while tile i is copied.
+    struct Row {
+      bool is, in_a;                                  // a tile of the unit; of the entries (else of the window)
+      int b, e[2], at[2], id[2];                      // sequence; entry (or the window's row), -1 = none; its row in the page; page id
+    };
+    const int cap = (int)paged_capacity(a);
+    int64_t t = 0;
+    bool more = seg.next(a);
+    if (more) t = seg.t0;
+    auto entry_of = [&]() {                           // the next tile: the entries
+      Row r{more, t < seg.ta, seg.b, {-1, -1}, {0, 0}, {0, 0}};
+      if (!more) return r;
+      const int v0 = (int)((r.in_a ? t : t - seg.ta) * PT_ROWS) + lane, n = r.in_a ? seg.na : seg.nw;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int v = v0 + 32 * u;
+        if (v < n) r.e[u] = !r.in_a ? seg.b * a.W + v : SPARSE ? a.idx[(size_t)seg.b * a.k + v] : v;
+      }
+      if (++t == seg.t1) {
+        more = seg.next(a);
+        t = seg.t0;
+      }
+      return r;
+    };
+    auto page_of = [&](Row r) {                       // their pages
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        r.id[u] = -1;
+        if (r.in_a && r.e[u] >= 0 && (!SPARSE || r.e[u] < cap)) {
+          const int pg = paged_page(a, r.e[u]);
+          r.at[u] = r.e[u] - pg * a.page;
+          r.id[u] = a.table[(size_t)r.b * a.table_w + pg];
+        }
+      }
+      return r;
+    };
+    // the rows of the pool or the window, -1 = none, and which there are
+    auto publish = [&](int i, const Row& r) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        int y = r.e[u];
+        if (r.in_a && y >= 0) {
+          if ((unsigned)r.id[u] < (unsigned)a.n_pages) y = r.id[u] * a.page + r.at[u];       // (a pool has less than 2^31 rows)
+          else { raise_err(a.err, CSA_DEVERR_INDEX); y = -1; }
+        }
+        sm.rowy[i & 1][lane + 32 * u] = y;            // (the copies of two tiles before are started)
+        const uint32_t vb = __ballot_sync(0xffffffffu, y >= 0);
+        if (lane == 0) sm.vmask[i & 3][u] = vb;
+      }
+    };
+    Row now = page_of(entry_of()), next = now, after = now;
+    if (now.is) publish(0, now);
+    for (int i = 0; now.is; ++i) {
+      named_bar(1, PT_LDT);
+      const int stop = *(volatile int*)&sm.ld_stop;
+      if (stop != 0 && stop <= i + 1) break;
+      if (i == 0) {                                   // (the first tile's copies wait for no other's rows)
+        next = entry_of();
+        after = entry_of();
+        next = page_of(next);
+      }
+      now = next;
+      next = page_of(after);
+      after = entry_of();
+      if (now.is) publish(i + 1, now);
+    }
   } else if (warp == PT_SW) {
     // ------------------------------------------------------------------ queries and S = Q K^T
     // The whole warp runs the loop (descriptors stay warp-uniform), one elected lane issues.  S
