@@ -4,29 +4,37 @@
 // Mathematics as in attention_paged.cu (an online softmax over 64-row tiles).  A CTA takes
 // 64 heads (the MMA M) and one unit of the schedule (paged.cuh): a run of tiles that may span
 // several sequences ("segments").  Per tile:
-//   1. the loader brings the 64 rows into a two-stage ring, in 128-byte swizzle atoms: runs of
-//      pages as TMA boxes of gcd(page, 64) rows, others (selected entries, pages that share no
-//      factor of 8 with 64, the last rows of a sequence) by tile::gather4.  Rows that are not
-//      attended are never copied: P = 0 there, but 0 * NaN must not reach the sums;
-//   2. one warp issues S = Q K^T (N = 64, 36 steps of K = 16) into TMEM;
+//   1. five warps bring the 64 rows, in 128-byte swizzle atoms: runs of pages as TMA boxes of
+//      gcd(page, 64) rows, others (selected entries, pages that share no factor of 8 with 64,
+//      the last rows of a sequence) by tile::gather4; another warp looks the rows up a tile
+//      ahead.  Dims 0-255 have a ring of two slots and dims 256-575 one of three.  Rows that are
+//      not attended are never copied: P = 0 there, but 0 * NaN must not reach the sums;
+//   2. one warp issues S = Q K^T (N = 64, 36 steps of K = 16) into TMEM.  The queries' dims 0-383
+//      are the A operand from TMEM (they come through a ring slot and tcgen05.cp, once per
+//      sequence), which leaves their 48 KB to the third slot;
 //   3. eight softmax warps read S, agree on the running maximum and write P to shared memory
 //      as two bf16 parts, P_hi = bf16(P) and P_lo = bf16(P - P_hi) (the second into the
 //      tile's rotary atom, which only S reads): P is held to 2^-17, where bf16 alone would
 //      add as much error as the rounding of the output;
-//   4. O += P_hi V + P_lo V (N = 2 x 256, V read MN-major from the same tile).
+//   4. O += P_hi V + P_lo V (N = 2 x 256, V read MN-major from the same tile), dims 0-255 first:
+//      their slot is the next that a load waits for.
 // The MMAs are the weight-stationary form at M = 64: O (64 x 512) takes 128 lanes x 256 columns
 // and S 128 lanes x 32 columns, so lane l and lane l + 64 hold halves of the same head.
 // At a segment's end O is normalised and stored, or left as a partial for the merge.
 // Every wait is bounded (CSA_DEVERR_TIMEOUT).
 //
-// Bound: at 64 heads HBM (two sequences of 131 072 rows: 73.6 us, 3.9 TB/s of 6.56 measured; a
-// CTA's two stages keep 144 KB in flight or at work), at 128 heads the operands that the MMAs of
-// two CTAs read from shared memory, 378 KB of 128 bytes a clock per tile and CTA (32 ragged
-// sequences: 105 us, 670 TFLOP/s), for gathered rows the gathers beside them (48 x 1152 rows:
-// 54.4 us, 2.5 us a tile), for one sequence latency (100 rows: 11.6 us).  A tile's chain is load
-// 0.65 us, S 0.55 + 0.15, softmax 0.4 + 0.25, hand-over 0.2, PV 0.65; two tiles overlap.
+// Bound: at 64 heads HBM (two sequences of up to 131 072 rows: 70 us, 4.1 TB/s of 6.56 measured,
+// start and merge included), at 128 heads the MMAs and the shared memory that they read (2432
+// cycles of MMAs a tile; 32 ragged sequences: 95.6 us, 740 TFLOP/s, 1.9 us a tile, of which a
+// tile's chain load 1.1 us, S 0.7, softmax 0.9, PV 0.8 is overlapped by two), for gathered rows
+// the gathers (48 x 1152 rows: 48.4 us, 2.4 us a tile: 30 GB/s beside the MMAs' operands, 55
+// alone), for one sequence latency (100 rows: 11.2 us).
+// Two slots for all dims and all queries in shared memory: 105 us ragged, 73.5 us for 64 heads.
 // Why 64 heads a CTA: O of 128 heads (512 columns) would leave no TMEM for S.  Why two bf16
 // parts of P: one part took 64 heads from 80 to 76 us when that was tried, for the error above.
+// Why few warps poll: all copying warps waiting on the slots' barriers made the ragged batch
+// 100 us, one thread and a named barrier 95.6; each test of a barrier goes through the shared
+// memory that the MMAs read.
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -48,8 +56,8 @@ constexpr int PT_LDW = 10;               // the warp that looks rows up
 constexpr int PT_CPW = 11;               // first of five that copy them
 constexpr int PT_CPT = 160, PT_LDT = 32 + PT_CPT;           // threads of the latter; of both
 constexpr int PT_THREADS = PT_CPW * 32 + PT_CPT;
-constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 12.6 us in one unit, 14.5 in two and a merge)
-constexpr int PT_BEGIN_COST = 2;         // (1: ragged batch 109.0 us, 2: 106.7, 3: 108.5)
+constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 11.3 us in one unit, 13.5 in two and a merge)
+constexpr int PT_BEGIN_COST = 2;         // (32 ragged sequences: 98.1 us at 1, 95.6 at 2, 97.9 at 3)
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
 constexpr int PT_QT = 6;                 // atoms of the queries that live in TMEM
@@ -62,16 +70,16 @@ struct PtSmem {
   uint8_t hi[3][PT_ATOMS - PT_LO][ATOM];     // 120 KB: dims 256-575 of three
   uint8_t p[PT_HC * 128];                    // P_hi: 64 heads x 64 rows bf16; between segments the row sums
   float smax[2][2][128];                     // per tile parity and warpgroup: the lanes' tile maxima
-  alignas(16) int rowy[2][PT_ROWS];                      // per stage: rows of the pool or the window, -1 = none
-  uint32_t vmask[4][2];                      // per tile mod 4 (the loader's warps may be three tiles ahead of the
-                                             // softmax): bit j of word j / 32 set when row j exists
+  alignas(16) int rowy[2][PT_ROWS];          // per tile mod 2: rows of the pool or the window, -1 = none
+  uint32_t vmask[4][2];                      // per tile mod 4 (a tile's are written when the softmax is past those of
+                                             // four tiles before): bit j of word j / 32 set when row j exists
   uint64_t lo_full[2], lo_empty[2], hi_full[3], hi_empty[3];
   uint64_t sfull[2], sfree[2];
   uint64_t pfull, pdone, qfull, qfree, ofree, drain[2];
   uint64_t headb[2], segb;                   // softmax warps: the four of the same heads; all eight
   uint32_t tmem_base;
   int abort_flag;
-  int ld_stop;                               // 1 + the tile at which the loader stops (0 = running)
+  int ld_stop;                               // 1 + the tile at which lookups and copies stop (0 = running)
 };
 static_assert(sizeof(PtSmem) <= 232448, "shared memory of one CTA (227 KB)");
 
@@ -223,9 +231,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
                 if (lane * rows < PT_ROWS)
                   tc::tma_load_2d(atom_of(at) + lane * rows * 128, in_a ? &maps.pages : &maps.win, half_full(x), 64 * at, sm.rowy[st][lane * rows]);
             } else {
-              // scattered rows by tile::gather4, four rows of 128 bytes an instruction.  One warp starts
-              // 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the issue slots
-              // and shared-memory ports that the softmax uses).  An absent row is a second copy of one
+              // scattered rows by tile::gather4, four rows of 128 bytes an instruction.  Alone, one warp
+              // starts 16 GB/s of them, six 55 (cp.async by as many threads: 46, and it needs the issue
+              // slots and shared-memory ports that the softmax uses).  An absent row is a second copy of one
               // that is there: its P is 0, and what it holds must not be less finite than the rest.
               const int there = sm.rowy[st][v0 ? __ffs(v0) - 1 : 31 + __ffs(v1)];
               const CUtensorMap* m = in_a ? &maps.rows : &maps.win_rows;
@@ -418,7 +426,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     tc::mbar_wait(&sm.drain[0], 0);
   } else if (warp == PT_PVW) {
     // ------------------------------------------------------------------ O (+)= (P_hi + P_lo) V
-    // Value dims 0-255 (atoms 0-3), then 256-511 (atoms 4-7), so that the first half of the stage
+    // Value dims 0-255 (atoms 0-3), then 256-511 (atoms 4-7), so that the slot of the first
     // is free early.  The two parts of P are two K ranges over the same V rows (a K step is 16
     // rows of 128 bytes).
     constexpr uint32_t ID_O = tc::idesc(tc::FMT_BF16, tc::FMT_BF16, PT_HC, 256, 0, 1);
@@ -596,7 +604,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
           tc::tmem_st_wait();
         }
         {
-          // P_lo goes to the stage's rotary atom: S of this tile, its only reader, is complete
+          // P_lo goes to the tile's rotary atom: S of this tile, its only reader, is complete
           const uint32_t pbase = tc::smem_u32(sm.p), lbase = tc::smem_u32(sm.hi[hi.at][PT_ATOMS - PT_LO - 1]);
           const int c0 = 4 * half + 2 * wg;           // 16-byte chunks (8 rows) of the head's P
 #pragma unroll

@@ -72,8 +72,8 @@ __host__ __device__ inline int64_t paged_capacity(const PagedAttnArgs& a) { retu
 // order, are dealt to the units in equal runs, so that every unit takes as long as the others
 // however ragged the lengths are; the lengths are read on the device only.  Beginning a sequence
 // costs a unit more than its tiles (queries, an empty pipeline, an epilogue): begin_cost places
-// that hold no tile come before a sequence's first one (tensor cores: 32 ragged sequences
-// 109.0 us at a cost of 1, 106.7 at 2, 108.5 at 3; fp32, where a tile costs as much: 0).  A sequence whose tiles lie in one unit is
+// that hold no tile come before a sequence's first one (tensor cores: 2;
+// CUDA cores, where a tile costs as much: 0).  A sequence whose tiles lie in one unit is
 // finished there; one that is cut leaves a partial (o, m, l) in each unit it touches, and a merge
 // kernel joins them.  A unit holds at most two partials: one of a sequence that began before it
 // (slot 0) and one of a sequence that begins in it and goes on (slot 1).
