@@ -248,8 +248,8 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
               }
             }
             __syncwarp();
-            if (x) ++n_hi; else ++n_lo;
           }
+          if (x) ++n_hi; else ++n_lo;
         }
         lo.step(2);
         hi.step(3);
@@ -260,7 +260,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     if (ct == 0)
       for (int q = 0; q < 5; ++q) {
         const int uses = q < 2 ? (n_lo + 1 - q) / 2 : (n_hi + 4 - q) / 3;      // of a ring's slot
-        if (uses > 0) tc::mbar_wait(q < 2 ? &sm.lo_full[q] : &sm.hi_full[q - 2], (uses - 1) & 1);
+        if (uses > 0 && !tc::mbar_wait(q < 2 ? &sm.lo_full[q] : &sm.hi_full[q - 2], (uses - 1) & 1)) atomicExch(&sm.abort_flag, 1);
       }
     __syncwarp();
   } else if (warp >= PT_LDW) {
@@ -423,7 +423,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     if (n > 0 || !ok) tc::mbar_wait(&sm.qfull, (ok ? n - 1 : n) & 1);
     if (tc::elect_one()) tc::mma_commit(&sm.drain[0]);
     __syncwarp();
-    tc::mbar_wait(&sm.drain[0], 0);
+    if (!tc::mbar_wait(&sm.drain[0], 0) && lane == 0) atomicExch(&sm.abort_flag, 1);
   } else if (warp == PT_PVW) {
     // ------------------------------------------------------------------ O (+)= (P_hi + P_lo) V
     // Value dims 0-255 (atoms 0-3), then 256-511 (atoms 4-7), so that the slot of the first
@@ -472,7 +472,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     if (!ok && lane == 0) atomicExch(&sm.abort_flag, 1);
     if (tc::elect_one()) tc::mma_commit(&sm.drain[1]);
     __syncwarp();
-    tc::mbar_wait(&sm.drain[1], 0);
+    if (!tc::mbar_wait(&sm.drain[1], 0) && lane == 0) atomicExch(&sm.abort_flag, 1);
   } else {
     // ------------------------------------------------------------------ softmax + epilogue, warps 0-7
     // Thread (wg, lane tl): head tl % 64; of S the tile rows 32 (tl / 64) + 16 wg .. + 15; of O

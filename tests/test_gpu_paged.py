@@ -12,6 +12,10 @@ Tolerances, per output value, u = 2^-24 (half a step of fp32):
 * bf16: the partials of a sequence cut over several CTAs are rounded to fp16 before they are
   joined, each by 2^-11 of itself at most (half a step: eps / 2), and their weighted magnitudes
   sum to at most A: 2^-11 A more;
+* bf16, d_v = 512: a quarter of a partial's dims shares a power of two s that puts its largest
+  magnitude into [s / 2, s), and below 2^-14 s the steps of fp16 stay at 2^-24 s: what is tiny is
+  rounded by 2^-25 s <= 2^-24 of the largest.  That is at most the partial's sum of p max |v| over
+  the quarter, and the partials' weighted sums add up to the sequence's: 2^-24 sum p max |v| more;
 * lse is off by D + (N + 16) * 2u + |lse| * 2u.
 """
 from __future__ import annotations
@@ -78,15 +82,18 @@ def reference(q, rows, sink, scale, dv):
     p = torch.exp(logits - safe[:, None])
     out = p @ rows[:, :dv]
     A = p @ rows[:, :dv].abs()
-    return out, lse, A, mag * (dk + 4) * 2 * U, N
+    if dv == 512 and N:
+        tiny = p @ rows[:, :dv].abs().view(N, 4, 128).amax(dim=2)
+        return out, lse, A, mag * (dk + 4) * 2 * U, N, 2.0 ** -24 * tiny.repeat_interleave(128, dim=1)
+    return out, lse, A, mag * (dk + 4) * 2 * U, N, 0.0
 
 
 def check(out, lse, q, rows_of, sink, scale, what=""):
     B, H, dv = out.shape
     for b in range(B):
-        o, l, A, D, N = reference(q[b], rows_of(b), sink, scale, dv)
+        o, l, A, D, N, tiny = reference(q[b], rows_of(b), sink, scale, dv)
         cut = 2.0 ** -11 if out.dtype == BF else 0.0
-        tol = A * (2 * D + 2.0 ** -15 + cut + 2 * (N + 16) * 2 * U)[:, None] + R[out.dtype] * o.abs()
+        tol = A * (2 * D + 2.0 ** -15 + cut + 2 * (N + 16) * 2 * U)[:, None] + R[out.dtype] * o.abs() + (tiny if out.dtype == BF else 0.0)
         bad = (out[b].double() - o).abs() > tol
         assert not bool(bad.any()) and bool(torch.isfinite(out[b]).all()), (
             what, b, N, float(((out[b].double() - o).abs() / tol.clamp(min=1e-300)).nan_to_num(9e9).max()))
@@ -142,8 +149,12 @@ class Case:
                                          self.scale, self.dv, self.out, self.lse, self.ws, stream=stream)
 
     def run_and_check(self, what=""):
+        t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        t[0].record()
         self.call()
+        t[1].record()
         torch.cuda.synchronize()
+        assert t[0].elapsed_time(t[1]) < 1000, "a device wait gave up (after 2 s)"
         assert csa.read_device_error() == 0
         check(self.out, self.lse, self.q, self.rows_of, self.sink, self.scale, what)
 
@@ -627,3 +638,14 @@ def test_the_most_sequences(dtype, dk, dv):
     tol = (p[:, None] * rows[:, :dv].abs()) * (2 * D + 2.0 ** -15 + 2.0 ** -11 * (dtype == BF) + 40 * U)[:, None] + R[dtype] * want.abs()
     assert bool(((out[:, 0].double() - want).abs() <= tol).all())
     assert bool(((lse[:, 0].double() - L).abs() <= D + 40 * U + L.abs() * 2 * U).all())
+
+
+@pytest.mark.parametrize("H", [128, 7])
+def test_tiles_without_a_row(H):
+    """Selections without an entry: whole tiles of zeros, alone and between others."""
+    idx = torch.full((5, 200), -1, dtype=torch.int32, device="cuda")
+    idx[1, 70:75] = torch.arange(5, dtype=torch.int32, device="cuda")
+    idx[3, ::3] = 7
+    idx[4, 199] = 300
+    Case(157, BF, H, 576, 512, 64, [400] * 5, 0, idx=idx).run_and_check("no window")
+    Case(163, BF, H, 576, 512, 64, [400] * 5, 9, idx=idx).run_and_check("window")
