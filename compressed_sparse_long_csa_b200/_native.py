@@ -325,7 +325,7 @@ def sparse_attn_decode_noalloc(q, cache, idx, win, win_len, sink, sm_scale, d_v,
 # checks are plain comparisons, written out (a helper per tensor cost 2 us a call); the message
 # is made when one fails.
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
-_device_now = torch.cuda.current_device
+_device_now = torch._C._cuda_getDevice      # (torch.cuda.current_device looks for an initialised context first)
 _stream_now = torch._C._cuda_getCurrentRawStream
 
 
