@@ -19,10 +19,10 @@ constexpr int PA_MAX_HALF = 288;       // rotated pairs of a row (d_r <= 576)
 constexpr int PA_THREADS = 128;
 // Query pieces that a thread loads first of all, and the heads of a CTA: few of both while the
 // grid does not fill the GPU (latency), many once it does (a token's entry, page and angles are
-// then looked up once).  bf16, 128 heads: 96 tokens 3.4 us against 4.9 the other way, 4096 tokens
-// 39.0 against 32.7 (4.3 TB/s; every ninth line of the query rows is written).
-constexpr int PA_FEW = 2, PA_MANY = 8;
-constexpr int PA_FEW_HEADS = 32;
+// then looked up once).  bf16, 128 heads: 96 tokens 3.3 us against 4.9 the other way, 4096 tokens
+// 39 against 32.8 (4.3 TB/s; every ninth line of the query rows is written).
+constexpr int PA_FEW = 1, PA_MANY = 8;   // (4: 35.4, 16: 38.4 us for the 4096; two pieces of 32 heads: one token 2.8 us, not 2.4)
+constexpr int PA_FEW_HEADS = 16;
 
 struct AppendArgs {
   const void* rows; int64_t rows_ld;
