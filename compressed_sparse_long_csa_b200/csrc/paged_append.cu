@@ -19,8 +19,8 @@ constexpr int PA_MAX_HALF = 288;       // rotated pairs of a row (d_r <= 576)
 constexpr int PA_THREADS = 128;
 // Query pieces that a thread loads first of all, and the heads of a CTA: few of both while the
 // grid does not fill the GPU (latency), many once it does (a token's entry, page and angles are
-// then looked up once).  bf16, 128 heads: 96 tokens 3.3 us against 4.9 the other way, 4096 tokens
-// 39 against 32.8 (4.3 TB/s; every ninth line of the query rows is written).
+// then looked up once).  bf16, 128 heads: 160 tokens 3.8 us against 5.0 the other way, 400
+// tokens 7.5 against 6.4; 4096 tokens 32.8 us (4.3 TB/s; every ninth line of the query rows is written).
 constexpr int PA_FEW = 1, PA_MANY = 8;   // (4: 35.4, 16: 38.4 us for the 4096; two pieces of 32 heads: one token 2.8 us, not 2.4)
 constexpr int PA_FEW_HEADS = 16;
 
@@ -154,7 +154,7 @@ cudaError_t launch_latent_append_paged(const void* rows, int64_t rows_ld, const 
                                        int dq, int dtype, cudaStream_t st, unsigned* err) {
   AppendArgs a{rows, rows_ld, seq, entry, pos, inv_freq, dr, pages, n_pages, page, table, table_w, B, T, d,
                q_pe, qpe_ld_t, qpe_ld_h, q, H, dq, q ? H : 1, err};
-  const bool few = q && (int64_t)T * ((H + PA_FEW_HEADS - 1) / PA_FEW_HEADS) <= 8 * num_sms();
+  const bool few = q && (int64_t)T * ((H + PA_FEW_HEADS - 1) / PA_FEW_HEADS) <= 12 * num_sms();
   if (few && H > PA_FEW_HEADS) a.heads = PA_FEW_HEADS;
   const dim3 grid(T, q ? (H + a.heads - 1) / a.heads : 1);
   note_launch();
