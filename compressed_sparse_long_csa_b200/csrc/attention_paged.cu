@@ -12,8 +12,6 @@
 // This path takes every shape and both storage types in fp32 arithmetic.
 #include "paged.cuh"
 
-#include <cuda_fp16.h>
-
 namespace csa {
 
 namespace {
@@ -283,9 +281,7 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
         float* blk = a.part + (size_t)seg.slot(unit) * paged_part_block(a.H, dv);
         *reinterpret_cast<float4*>(blk + paged_part_val(a.H, h, c)) = y;
         if (c == 0) {
-          float4* rec = reinterpret_cast<float4*>(blk + paged_part_rec(a.H, dv, h));
-          rec[0] = make_float4(M, l, 1.f, 1.f);
-          rec[1] = make_float4(1.f, 1.f, 0.f, 0.f);
+          *reinterpret_cast<float2*>(blk + paged_part_rec(a.H, dv, h)) = make_float2(M, l);
         }
       }
     }
@@ -298,54 +294,36 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
 // every CTA gathers those notes and takes its share of the items (sequence, eight heads,
 // slice of the dims), the slices as narrow as it takes to give every CTA an item.  Eight
 // heads' 16-byte pieces of a partial are one 128-byte line.  Where a slice leaves threads
-// over, they share its pieces.  All sums run in a fixed order, so a result does not depend
+// over, they share its partials.  All sums run in a fixed order, so a result does not depend
 // on the order in which the units ended.  Bound: latency (the notes, the records, the partials:
-// three round trips and the launch, 4 to 6 us behind the attention) and the L2, H * (2 or 4 dv +
-// 32) bytes per piece.  Sequences of few partials are a warp's work, so that many of them run at
+// three round trips and the launch, 4 to 6 us behind the attention) and the L2, 4 H (dv + 4)
+// bytes per piece.  Sequences of few partials are a warp's work, so that many of them run at
 // once (32 ragged sequences 109.5 us without, 106.3 with; sparse, 48 sequences 58.7 against 55.9).
 constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16;
-constexpr int PM_EARLY = 5;      // partials on their way at once (9: 64 heads 73.4 -> 73.9 us)
+constexpr int PM_EARLY = 5;      // partials on their way at once (9: two sequences of 131 072 rows, 64 heads 71.3 -> 71.9 us)
 constexpr int PM_PER_SM = 2;     // (1: 32 ragged sequences 105.0 -> 107.5 us)
-constexpr int PM_FEW = 8;        // partials that one warp joins by itself
+constexpr int PM_FEW = 8;        // partials that one warp joins by itself (4: 32 ragged sequences 98.9 -> 100.4 us)
 constexpr int PM_ROUNDS = 2;     // notes of a thread: up to 512 units
 // Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)
-constexpr size_t pm_unit_bytes(bool part16) { return PM_H * (sizeof(float4) + (part16 ? sizeof(float2) : 0)) + sizeof(int4); }
+constexpr size_t PM_UNIT_BYTES = PM_H * sizeof(float2) + sizeof(int4);
 // acc += w times a 16-byte piece of a partial
-template <bool PART16>
-__device__ __forceinline__ void merge_add(float* acc, const uint4& v, float w) {
-  const uint32_t u4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if constexpr (PART16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u4[q]));
-      acc[2 * q] = fmaf(w, f.x, acc[2 * q]);
-      acc[2 * q + 1] = fmaf(w, f.y, acc[2 * q + 1]);
-    } else {
-      acc[q] = fmaf(w, __uint_as_float(u4[q]), acc[q]);
-    }
-  }
+__device__ __forceinline__ void merge_add(float4& acc, const float4& v, float w) {
+  acc = make_float4(fmaf(w, v.x, acc.x), fmaf(w, v.y, acc.y), fmaf(w, v.z, acc.z), fmaf(w, v.w, acc.w));
 }
-template <typename T, int V>
-__device__ __forceinline__ void merge_store(T* dst, const float* v) {
-  if constexpr (V == Elem<T>::VEC) {
-    Elem<T>::st_vec(dst, v);
-  } else {
-#pragma unroll
-    for (int u = 0; u < V; ++u) Elem<T>::st(dst + u, v[u]);
-  }
+__device__ __forceinline__ void merge_store(float* dst, const float4& v) { *reinterpret_cast<float4*>(dst) = v; }
+__device__ __forceinline__ void merge_store(__nv_bfloat16* dst, const float4& v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <typename T, bool PART16>
+template <typename T>
 __global__ void __launch_bounds__(PM_THREADS, PM_PER_SM)
 paged_merge_kernel(PagedAttnArgs a) {
-  constexpr int V = PART16 ? 8 : 4;                  // dims of a 16-byte piece
-  // per unit: the list {unit, sequence, partials, -}; per partial and head: {m, l, s0, s1}, then
-  // e^{m - M} times the quarters' powers, and {s2, s3}
+  // per unit: the list {unit, sequence, partials, -}; per partial and head: {m, l}, then {e^{m - M}, l}
   extern __shared__ int4 list[];
-  float4* const wts = reinterpret_cast<float4*>(list + a.units);
-  float2* const s23 = reinterpret_cast<float2*>(wts + (size_t)a.units * PM_H);
+  float2* const wts = reinterpret_cast<float2*>(list + a.units);
   __shared__ float red[2][PM_THREADS / 32][PM_H];
-  __shared__ float sums[V][PM_THREADS];
+  __shared__ float4 sums[PM_THREADS];
   __shared__ int counts[PM_ROUNDS * PM_THREADS / 32];
   const int dv = a.dv, H = a.H;
   const int hl = threadIdx.x & (PM_H - 1), j = threadIdx.x / PM_H;
@@ -382,7 +360,7 @@ paged_merge_kernel(PagedAttnArgs a) {
   }
   __syncthreads();
   const int n_few = all & 0xffff, count = all >> 16;
-  const int hb = (H + PM_H - 1) / PM_H, pieces = dv / V;
+  const int hb = (H + PM_H - 1) / PM_H, pieces = dv / 4;    // 16-byte pieces of a head's o
   int slices = 1;
   while (slices < PM_SLICES && 2 * count * hb * slices <= (int)gridDim.x && pieces / slices > 4) slices <<= 1;
   const int width = (pieces + slices - 1) / slices;   // 16-byte pieces of a slice
@@ -399,14 +377,14 @@ paged_merge_kernel(PagedAttnArgs a) {
       const int hc = hv ? h : H - 1;
       const float* part = a.part + (size_t)(2 * cut.x) * block;
       auto partial = [&](int p) { return part + (p ? 2 * p * block : block); };
-      uint4 x[2][4];                                  // four partials' pieces; the first four's are on their way
+      float4 x[2][4];                                 // four partials' pieces; the first four's are on their way
       auto load = [&](int p0) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int c = cg * 8 + 4 * k + q;
-            if (p0 + u < n && c < pieces) x[k][u] = __ldcg(reinterpret_cast<const uint4*>(partial(p0 + u)) + (size_t)c * H + hc);
+            if (p0 + u < n && c < pieces) x[k][u] = __ldcg(reinterpret_cast<const float4*>(partial(p0 + u)) + (size_t)c * H + hc);
           }
         }
       };
@@ -419,10 +397,8 @@ paged_merge_kernel(PagedAttnArgs a) {
         const int p = q + 4 * k;
         m[k] = -INFINITY;
         l[k] = 0.f;
-        w[k] = 1.f;
         if (p < n) {
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(partial(p) + rec));
-          if (PART16) w[k] = __ldcg(partial(p) + rec + 2 + ((cg * 8) >> 4));      // 16 pieces a quarter
           m[k] = ml.x;
           l[k] = ml.y;
         }
@@ -435,17 +411,13 @@ paged_merge_kernel(PagedAttnArgs a) {
       for (int k = 0; k < 2; ++k) {
         const float e = m[k] == -INFINITY ? 0.f : __expf(m[k] - M);
         den += e * l[k];
-        w[k] *= e;
+        w[k] = e;
       }
       den += __shfl_xor_sync(0xffffffffu, den, 8);
       den += __shfl_xor_sync(0xffffffffu, den, 16);
       den += sk == -INFINITY ? 0.f : __expf(sk - M);
       const float inv = den > 0.f ? 1.f / den : 0.f;
-      float acc[2][V];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int u = 0; u < V; ++u) acc[k][u] = 0.f;
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 1
       for (int p0 = 0; p0 < n; p0 += 4) {
         if (p0) load(p0);
@@ -454,14 +426,14 @@ paged_merge_kernel(PagedAttnArgs a) {
           if (p0 + u < n) {
             const float wu = __shfl_sync(0xffffffffu, p0 ? w[1] : w[0], hl + 8 * u) * inv;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) merge_add<PART16>(acc[k], x[k][u], wu);
+            for (int k = 0; k < 2; ++k) merge_add(acc[k], x[k][u], wu);
           }
         }
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int c = cg * 8 + 4 * k + q;
-        if (hv && c < pieces) merge_store<T, V>((T*)a.out + ((size_t)b * H + h) * dv + V * c, acc[k]);
+        if (hv && c < pieces) merge_store((T*)a.out + ((size_t)b * H + h) * dv + 4 * c, acc[k]);
       }
       if (a.lse && cg == 0 && q == 0 && hv) a.lse[(size_t)b * H + h] = den == 0.f ? -INFINITY : M + logf(den);
     }
@@ -478,34 +450,23 @@ paged_merge_kernel(PagedAttnArgs a) {
     // partial 0 lies in slot 1 of the unit, partial p > 0 in slot 0 of unit + p
     const float* part = a.part + (size_t)(2 * cut.x) * block;
     auto partial = [&](int p) { return part + (p ? 2 * p * block : block); };
-    auto load = [&](int p, int c) { return __ldcg(reinterpret_cast<const uint4*>(partial(p)) + (size_t)c * H + hc); };
+    auto load = [&](int p, int c) { return __ldcg(reinterpret_cast<const float4*>(partial(p)) + (size_t)c * H + hc); };
     const size_t rec = paged_part_rec(H, dv, hc);
     const float sk = a.sink[hc];
-    float acc[V];
     const int cend = min(pieces, (sl + 1) * width);
     const int c0 = sl * width + jc;
     float M = sk;
     for (int p0 = j; p0 < n; p0 += 4 * PM_C) {        // four records' loads at a time
-      float4 r0[4];
-      float2 r1[4];
+      float2 r[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int p = p0 + u * PM_C;
-        if (p < n) {
-          const float4* r = reinterpret_cast<const float4*>(partial(p) + rec);
-          r0[u] = __ldcg(r);
-          if (PART16) r1[u] = __ldcg(reinterpret_cast<const float2*>(r + 1));
-        }
-      }
+      for (int u = 0; u < 4; ++u)
+        if (p0 + u * PM_C < n) r[u] = __ldcg(reinterpret_cast<const float2*>(partial(p0 + u * PM_C) + rec));
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int p = p0 + u * PM_C;
-        if (p < n) {
-          wts[p * PM_H + hl] = r0[u];
-          if (PART16) s23[p * PM_H + hl] = r1[u];
-          M = fmaxf(M, r0[u].x);
+      for (int u = 0; u < 4; ++u)
+        if (p0 + u * PM_C < n) {
+          wts[(p0 + u * PM_C) * PM_H + hl] = r[u];
+          M = fmaxf(M, r[u].x);
         }
-      }
     }
 #pragma unroll
     for (int o = PM_H; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -515,15 +476,10 @@ paged_merge_kernel(PagedAttnArgs a) {
     for (int w = 0; w < PM_THREADS / 32; ++w) M = fmaxf(M, red[0][w][hl]);
     float den = 0.f;
     for (int p = j; p < n; p += PM_C) {
-      const float4 r = wts[p * PM_H + hl];            // this thread's own
+      const float2 r = wts[p * PM_H + hl];            // this thread's own
       const float w = r.x == -INFINITY ? 0.f : __expf(r.x - M);
       den += w * r.y;
-      if (PART16) {
-        const float2 s = s23[p * PM_H + hl];
-        wts[p * PM_H + hl] = make_float4(w * r.z, w * r.w, w * s.x, w * s.y);
-      } else {
-        wts[p * PM_H + hl].x = w;
-      }
+      wts[p * PM_H + hl].x = w;
     }
 #pragma unroll
     for (int o = PM_H; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -534,34 +490,26 @@ paged_merge_kernel(PagedAttnArgs a) {
     for (int w = 0; w < PM_THREADS / 32; ++w) den += red[1][w][hl];
     const float inv = den > 0.f ? 1.f / den : 0.f;
     for (int c = c0; c - jc < cend; c += gw) {
-#pragma unroll
-      for (int u = 0; u < V; ++u) acc[u] = 0.f;
-      const float* wq = reinterpret_cast<const float*>(wts + hl) + (PART16 ? (c >> 4) & 3 : 0);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < cend) {
 #pragma unroll 1
         for (int p0 = g; p0 < n; p0 += PM_EARLY * groups) {
-          uint4 x[PM_EARLY];
+          float4 x[PM_EARLY];
 #pragma unroll
           for (int u = 0; u < PM_EARLY; ++u)
             if (p0 + u * groups < n) x[u] = load(p0 + u * groups, c);
 #pragma unroll
           for (int u = 0; u < PM_EARLY; ++u)
-            if (p0 + u * groups < n) merge_add<PART16>(acc, x[u], wq[(p0 + u * groups) * PM_H * 4]);
+            if (p0 + u * groups < n) merge_add(acc, x[u], wts[(p0 + u * groups) * PM_H + hl].x);
         }
       }
       if (groups > 1) {                               // (the slice is one round of its threads)
-#pragma unroll
-        for (int u = 0; u < V; ++u) sums[u][threadIdx.x] = acc[u];
+        sums[threadIdx.x] = acc;
         __syncthreads();
-        for (int o = 1; g == 0 && o < groups; ++o)
-#pragma unroll
-          for (int u = 0; u < V; ++u) acc[u] += sums[u][threadIdx.x + o * gw * PM_H];
+        for (int o = 1; g == 0 && o < groups; ++o) merge_add(acc, sums[threadIdx.x + o * gw * PM_H], 1.f);
       }
-      if (g == 0 && c < cend && hv) {
-#pragma unroll
-        for (int u = 0; u < V; ++u) acc[u] *= inv;
-        merge_store<T, V>((T*)a.out + ((size_t)b * H + h) * dv + V * c, acc);
-      }
+      if (g == 0 && c < cend && hv)
+        merge_store((T*)a.out + ((size_t)b * H + h) * dv + 4 * c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     }
     if (a.lse && j == 0 && sl == 0 && hv) a.lse[(size_t)b * H + h] = den == 0.f ? -INFINITY : M + logf(den);
     __syncthreads();                                  // the weights and sums are read
@@ -570,7 +518,7 @@ paged_merge_kernel(PagedAttnArgs a) {
 
 }  // namespace
 
-cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, cudaStream_t st) {
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
   if (a.units > PM_ROUNDS * PM_THREADS) return cudaErrorInvalidConfiguration;
   if (a.units == 1) return cudaSuccess;                // nothing is ever cut
   const int64_t most = (int64_t)(a.units - 1) * ((a.H + PM_H - 1) / PM_H) * PM_SLICES;
@@ -578,7 +526,7 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(most < grid ? most : grid));
   cfg.blockDim = dim3(PM_THREADS);
-  cfg.dynamicSmemBytes = (size_t)a.units * pm_unit_bytes(part16);            // a sequence has at most `units` partials
+  cfg.dynamicSmemBytes = (size_t)a.units * PM_UNIT_BYTES;            // a sequence has at most `units` partials
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the pieces first of all
@@ -586,9 +534,8 @@ cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, c
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   note_launch();
-  if (part16) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, true>, a);
-  return dtype == CSA_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16, false>, a)
-                           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<float, false>, a);
+  return dtype == CSA_BF16 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, a)
+                           : cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, a);
 }
 
 // Two CTAs per SM over the head groups.
@@ -626,7 +573,7 @@ cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st) {
     kerns[at]<<<grid, PC_WARPS * 32, bufs * tile + qs, st>>>(a, bufs, log_g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_paged_merge(a, dtype, false, st);
+    return launch_paged_merge(a, dtype, st);
   };
   return dtype == CSA_BF16 ? go(__nv_bfloat16()) : go(float());
 }

@@ -38,7 +38,6 @@
 #include "paged.cuh"
 #include "tc.cuh"
 
-#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 namespace csa {
@@ -643,25 +642,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         f = den > 0.f ? e / den : 0.f;
       }
       const int d0 = 256 * wg + 128 * half;
-      if (!seg.whole) {
-        // the power of two that puts the quarter's largest magnitude in [0.5, 1)
-        float amax = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[64];
-          tc::tmem_ld64(tmem + lane_base + TM_O + 128 * wg + c * 64, v);
-#pragma unroll
-          for (int j = 0; j < 64; ++j) amax = fmaxf(amax, fabsf(__uint_as_float(v[j])));
-        }
-        int e2 = 0;
-        frexpf(amax, &e2);
-        f = ldexpf(1.f, -e2);
-        if (hv) {
-          float* rec = blk + paged_part_rec(a.H, 512, h);
-          rec[2 + 2 * wg + half] = ldexpf(1.f, e2);
-          if (wg == 0 && half == 0) *reinterpret_cast<float2*>(rec) = make_float2(m, l);
-        }
-      }
+      if (!seg.whole && hv && wg == 0 && half == 0) *reinterpret_cast<float2*>(blk + paged_part_rec(a.H, 512, h)) = make_float2(m, l);
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t v[64];
@@ -674,7 +655,6 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         }
         if (!hv) continue;
         __nv_bfloat16* o = (__nv_bfloat16*)a.out + ((size_t)seg.b * a.H + h) * 512 + d0 + c * 64;
-        uint4* p16 = reinterpret_cast<uint4*>(blk) + (size_t)((d0 + c * 64) / 8) * a.H + h;
         if (seg.whole) {
           // each lane has a row of its own: whole sectors, or the store's lines cost as much again
 #pragma unroll
@@ -688,16 +668,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
             st_global32(o + q * 16, w, wide);
           }
         } else {
+          uint4* part = reinterpret_cast<uint4*>(blk + paged_part_val(a.H, h, d0 + c * 64));
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 hf = __floats2half2_rn(__uint_as_float(v[q * 8 + 2 * j]) * f, __uint_as_float(v[q * 8 + 2 * j + 1]) * f);
-              w[j] = *reinterpret_cast<const uint32_t*>(&hf);
-            }
-            p16[(size_t)q * a.H] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int q = 0; q < 16; ++q) part[(size_t)q * a.H] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
       }
       __syncwarp();
@@ -785,7 +758,7 @@ cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st) {
   note_launch();
   e = cudaLaunchKernelEx(&cfg, kern, maps, a, halves, box);
   if (e != cudaSuccess) return e;
-  return launch_paged_merge(a, CSA_BF16, true, st);
+  return launch_paged_merge(a, CSA_BF16, st);
 }
 
 }  // namespace csa

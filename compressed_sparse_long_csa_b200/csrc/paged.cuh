@@ -188,20 +188,15 @@ struct PagedSeg {
   __device__ __forceinline__ int slot(int unit) const { return 2 * unit + (t0 == 0 ? 1 : 0); }
 };
 
-// A partial of a cut sequence holds o (not normalised), m and l per head, for natural-log
-// logits, in one of two forms:
-//   fp32 (CUDA-core kernel): o as [dv / 4][H][4], then records [H][8] {m, l, 1, 1, 1, 1, -, -};
-//   fp16 (tensor-core kernel, dv = 512): o as [dv / 8][H][8], each quarter of the dims (128) of
-//     a head divided by the power of two that puts its largest magnitude in [0.5, 1), then
-//     records {m, l, s0 .. s3, -, -} with those powers.  A stored value is off by 2^-11 of
-//     itself at most (by 2^-25 of the quarter's largest where it is tiny), an eighth of the
-//     rounding of the bf16 output, and a partial's bytes halve, which cross the L2 twice (four
-//     sequences of 8192 rows: 46 -> 39 us).
-// Consecutive heads store contiguous 16-byte pieces in both.
-__host__ __device__ inline size_t paged_part_block(int H, int dv) { return (size_t)H * (dv + 8); }      // floats
+// A partial of a cut sequence holds o (not normalised), m and l per head, for natural-log logits, in
+// fp32: o as [dv / 4][H][4], then records [H][4] {m, l, -, -}.  Consecutive heads store contiguous
+// 16-byte pieces.  (o in fp16 with a power of two per 128 dims halves the bytes, which cross the L2
+// twice - 4 sequences of 8192 rows 31.8 us instead of 33.1, 32 ragged ones 96.0 instead of 98.9 - but
+// rounds each piece's sums by up to 2^-11 before they are joined, and some percent of the bf16 outputs
+// then come out a step away from the rounded sum.)
+__host__ __device__ inline size_t paged_part_block(int H, int dv) { return (size_t)H * (dv + 4); }      // floats
 __host__ __device__ inline size_t paged_part_val(int H, int h, int c) { return ((size_t)(c >> 2) * H + h) * 4 + (c & 3); }
-__host__ __device__ inline size_t paged_part_val16(int H, int h, int c) { return ((size_t)(c >> 3) * H + h) * 8 + (c & 7); }
-__host__ __device__ inline size_t paged_part_rec(int H, int dv, int h) { return (size_t)dv * H + 8 * (size_t)h; }
+__host__ __device__ inline size_t paged_part_rec(int H, int dv, int h) { return (size_t)dv * H + 4 * (size_t)h; }
 
 // After the partials, one note per unit: {b, n} when sequence b begins in the unit and goes on
 // in the n - 1 units after it, {-, 0} otherwise.
@@ -264,8 +259,8 @@ inline int64_t paged_rows_max(const PagedAttnArgs& a) { return (a.idx ? (int64_t
 int paged_units_cc(int B, int H, int64_t rows_max);
 int paged_units_tc(int B, int H, int64_t rows_max);
 
-// Joins the pieces of cut sequences (a.units, a.tile and a.min_tiles as in the attention launch).
-cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, bool part16, cudaStream_t st);
+// Joins the pieces of cut sequences (a.units as in the attention launch, whose notes name them).
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int dtype, cudaStream_t st);
 cudaError_t launch_paged_attn_cc(PagedAttnArgs a, int dtype, cudaStream_t st);
 // bf16, d_k = 576, d_v = 512 only.
 cudaError_t launch_paged_attn_tc(PagedAttnArgs a, cudaStream_t st);
