@@ -624,6 +624,9 @@ attn_tc_kernel(const __grid_constant__ AtMaps maps, AttnArgs a) {
       const float inv_l = (have_o && l_h > 0.f) ? 1.f / l_h : 0.f;
       int e2 = 0;
       frexpf(amax * inv_l, &e2);
+      // 2^e2 and 2^-e2 are both to be finite: smaller values keep steps of 2^-150 (bf16's own end at
+      // 2^-133), larger ones are below 4 in fp16
+      e2 = max(-126, min(126, e2));
       const float f = inv_l * ldexpf(1.f, -e2);
       uint4* d16 = reinterpret_cast<uint4*>(blk) + h;
 #pragma unroll 1
