@@ -57,7 +57,7 @@ constexpr int PT_CPT = 160, PT_LDT = 32 + PT_CPT;           // threads of the la
 constexpr int PT_THREADS = PT_CPW * 32 + PT_CPT;
 constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 11.3 us in one unit, 13.5 in two and a merge)
 constexpr int PT_BEGIN_COST = 2;         // (32 ragged sequences: 98.1 us at 1, 95.6 at 2, 97.9 at 3)
-constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum grows 256-fold
+constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum has grown 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
 constexpr int PT_QT = 6;                 // atoms of the queries that live in TMEM
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_Q = 320, TM_COLS = 512;    // TMEM columns: O 256, S 2 x 32, queries 6 x 32
@@ -490,7 +490,8 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (lane == 0) tc::mbar_arrive(&sm.segb);
       return __all_sync(0xffffffffu, tc::mbar_wait(&sm.segb, met++ & 1));
     };
-    // logits in the base-2 domain: P = 2^(s - m)
+    // logits in the base-2 domain: P = 2^(s - m), m set to PT_RESCALE above the maximum, so that P <= 1
+    // while O is not rescaled: sums of values come no nearer to the type's end than the formula's
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     const float scale2 = a.sm_scale * 1.4426950408889634f;
     const float scale = fmaxf(fabsf(scale2), 1.2e-38f);          // not 0: an absent row's -inf must stay one
@@ -550,7 +551,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
         for (int j = 4; j < 16; ++j) mq[j & 3] = fmaxf(mq[j & 3], s[j]);
         float mt = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * scale;
         // The tile's maximum over the head's four threads.  P is formed with the maximum so
-        // far while theirs arrive, and once more where it has to rise (lazily, by 2^8 at least).
+        // far while theirs arrive, and once more where it has to rise.
         float* const mx = sm.smax[st][0];
         mx[wg * 128 + tl] = mt;
         __syncwarp();
@@ -575,10 +576,10 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
           if (!__all_sync(0xffffffffu, tc::mbar_wait(headb, i & 1))) { ok = false; break; }
           met_all = true;
           mt = fmaxf(fmaxf(mx[hl], mx[hl + 64]), fmaxf(mx[hl + 128], mx[hl + 192]));
-          const bool raise = mt > m_run + PT_RESCALE || (m_run == -INFINITY && mt != -INFINITY);
+          const bool raise = mt > m_run;
           if (!__any_sync(0xffffffffu, raise)) break;
           if (raise) {
-            const float m_new = fmaxf(mt, m_run);
+            const float m_new = mt + PT_RESCALE;
             alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
             rescale = m_run != -INFINITY;
             m_run = m_new;

@@ -36,6 +36,7 @@ class Plain(Case):
 
     def put(self, b, ids, dims, x):
         """rows[ids][:, dims] = x of sequence b"""
+        assert 0 <= int(ids.min()) and int(ids.max()) < self.lens[b]
         ids = ids.cuda()
         self.pages[self.table[b].long()[ids // 64], ids % 64, dims] = x if isinstance(x, float) else x.to(self.pages)
 
@@ -106,3 +107,19 @@ def test_pieces_are_joined_without_another_rounding(lens, dtype, H, dk, dv):
         want = rows.mean(dim=0).float().to(BF)
         assert torch.equal(c.out[b], want.expand(H, dv)), (b, int((c.out[b] != want).sum()))
         assert bool(((c.lse[b].double() - math.log(n)).abs() <= 4 * U * math.log(n)).all())
+
+
+@pytest.mark.parametrize("dtype,H,dk,dv", SHAPES)
+@pytest.mark.parametrize("lens", [[100, 64], [20000, 15000, 9000, 12000]])
+@pytest.mark.parametrize("nats", [-3.0, 0.7, 5.4, 20.0])
+def test_large_values_at_a_maximum_that_rises(nats, lens, dtype, H, dk, dv):
+    """Values of 2^126 in a row behind others of lower or higher logits: the sums of p v, p <= 1, are in range."""
+    c = Plain(23, dtype, H, dk, dv, lens)
+    dims = torch.arange(dv // 4, dv // 2)
+    for b, n in enumerate(lens):
+        c.put(b, torch.arange(n)[:, None], dims.cuda(), 0.0)
+        at = torch.tensor([min(n - 1, n // 2 + 30 + 64 * b)])      # (not every unit begins at that tile)
+        c.put(b, at, dims.cuda(), (1.0 + (dims % 100) / 128.0) * (1 - 2 * (dims % 2)) * 2.0 ** 126)
+        c.put(b, at, dk - 1, nats)
+    c.run()
+    c.check(nats)
