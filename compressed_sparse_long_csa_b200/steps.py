@@ -19,6 +19,8 @@ calls; every number is computed by the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -83,12 +85,14 @@ def _ifmt(D):
 def page_caches(T, D, kind, page_size=64):
     """Move the entry caches of an uploaded decode workload into pages.  T gets, per cache, the pool
     "pages" and its "block_table" (room for the contiguous cache's entries), the rows "fresh" that a
-    step pools its entry into, where these go ("fresh_seq", "fresh_entry") and the workspace of the
-    paged attention.  The decode steps then use these; the contiguous cache is left alone."""
+    step pools its entry into, where these go ("fresh0", "fresh_seq", "fresh_entry"; set by every step
+    from the "entry0" it finds on the device, so that a program or a replayed graph moves on by writing
+    that) and the workspace of the paged attention.  The decode steps then use these; the contiguous
+    cache is left alone."""
     for p, csa in (("", kind != "hca_decode"), ("h_", False)):
         if p + "cache" not in T:
             continue
-        cache, entry0 = T[p + "cache"], T[p + "entry0"]
+        cache = T[p + "cache"]
         B, n_max, d = cache.shape
         i32 = dict(dtype=torch.int32, device=cache.device)
         width = -(-n_max // page_size)
@@ -98,26 +102,43 @@ def page_caches(T, D, kind, page_size=64):
         T[p + "block_table"] = torch.arange(B * width, **i32).view(B, width)
         rows = 2 if csa else 1
         T[p + "fresh"] = torch.zeros(B, rows, d, dtype=cache.dtype, device=cache.device)
+        T[p + "fresh0"] = torch.zeros(B, **i32)
         T[p + "fresh_seq"] = torch.arange(B, **i32).repeat_interleave(rows)
         if csa:
-            # the CSA pooling takes its entry's index from where it writes (entry 0 has no block
-            # before it): row 0 for a sequence's first entry, row 1 for any other; the row that
-            # is not written is no entry of the cache (-1)
-            first = entry0 == 0
-            T[p + "fresh0"] = entry0.clamp(max=1)
-            T[p + "fresh_entry"] = torch.stack((torch.where(first, 0, -1), torch.where(first, -1, entry0)), 1).to(torch.int32).view(-1)
-        else:
-            T[p + "fresh0"] = torch.zeros(B, **i32)
-            T[p + "fresh_entry"] = entry0.clone()
+            T[p + "fresh_row"] = torch.arange(rows, **i32).repeat(B, 1)
+            T[p + "fresh_is"] = torch.zeros(B, rows, dtype=torch.bool, device=cache.device)
+            T[p + "fresh_none"] = torch.full((1,), -1, **i32)
+            T[p + "fresh_entry"] = torch.full((B, rows), -1, **i32)
         attended = (D["k"] if csa else width * page_size) + D["W"]
         T[p + "paws"] = torch.empty(N.attn_decode_paged_workspace_size(B, D["H"], D["dv"], attended), dtype=torch.uint8,
                                     device=cache.device)
 
 
+def _place_fresh(T, p, stream):
+    """Where the step's entry is pooled to and which row of the pages it becomes, from the entry0 of
+    this moment (a few device operations on buffers, so that a captured step follows it).  An entry0
+    below 0 stays below 0 and is refused by the pooling, as in the contiguous steps."""
+    entry0 = T[p + "entry0"]
+    on = contextlib.nullcontext()
+    if stream is not None:
+        on = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    with on:
+        if p + "fresh_row" in T:
+            # the CSA pooling takes its entry's index from where it writes (entry 0 has no block
+            # before it): row 0 for a sequence's first entry, row 1 for any other; the row that
+            # is not written is no entry of the cache (-1)
+            torch.clamp(entry0, max=1, out=T[p + "fresh0"])
+            torch.eq(T[p + "fresh_row"], T[p + "fresh0"][:, None], out=T[p + "fresh_is"])
+            torch.where(T[p + "fresh_is"], entry0[:, None], T[p + "fresh_none"], out=T[p + "fresh_entry"])
+        else:
+            torch.clamp(entry0, max=0, out=T[p + "fresh0"])
+
+
 def _append_fresh(T, p, stream):
     fresh = T[p + "fresh"]
-    N.latent_append_paged(fresh.view(-1, fresh.shape[2]), T[p + "fresh_entry"], T[p + "pages"], T[p + "block_table"],
-                          seq=T[p + "fresh_seq"], stream=stream)
+    entry = T[p + "fresh_entry"].view(-1) if p + "fresh_entry" in T else T[p + "entry0"]
+    N.latent_append_paged(fresh.view(-1, fresh.shape[2]), entry, T[p + "pages"], T[p + "block_table"], seq=T[p + "fresh_seq"],
+                          stream=stream)
 
 
 _SIDE = {}
@@ -172,6 +193,7 @@ def _csa_layer(T, D, stream, attend):
 
 def _csa_decode_paged_step(T, D, stream):
     """csa_decode_step with the entries in pages (page_caches)."""
+    _place_fresh(T, "", stream)
     N.csa_compress(T["Ca"], T["Cb"], T["Za"], T["Zb"], T["Ba"], T["Bb"], T["prev_Cb"], T["prev_Zb"], T["fresh0"],
                    T["fresh"], m=D["m"], stream=stream)
     _append_fresh(T, "", stream)
@@ -202,6 +224,7 @@ def hca_decode_step(T, D, stream=None, prefix=""):
     if p + "raw_new" in T:
         N.window_append(T[p + "raw_new"], T[p + "win"], T["win_slot"], stream=stream)
     if p + "pages" in T:
+        _place_fresh(T, p, stream)
         N.hca_compress(T[p + "C"], T[p + "Z"], T[p + "bias"], T[p + "fresh0"], T[p + "fresh"], m_prime=D["m_prime"],
                        stream=stream)
         _append_fresh(T, p, stream)
