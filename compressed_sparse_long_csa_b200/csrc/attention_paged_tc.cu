@@ -349,9 +349,11 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     }
     bool ok = true;
     int n = 0, i = 0;
+    tc::ArmedLoads queries;
     for (; ok && seg.next(a); ++n) {
       // the segment before no longer reads Q once its last S is complete
       if (n > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.qfree, (n - 1) & 1))) { ok = false; break; }
+      queries.arm();
       if (tc::elect_one()) {
         tc::mbar_arrive_expect_tx(&sm.qfull, (PT_ATOMS - PT_QT) * PT_HC * 128);
         for (int at = PT_QT; at < PT_ATOMS; ++at)
@@ -419,7 +421,7 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
     }
     if (!ok && lane == 0) atomicExch(&sm.abort_flag, 1);
     // no copy of the queries and no MMA is in flight when the CTA frees TMEM and exits
-    if (n > 0 || !ok) tc::mbar_wait(&sm.qfull, (ok ? n - 1 : n) & 1);
+    if (queries.any()) tc::mbar_wait(&sm.qfull, queries.last());
     if (tc::elect_one()) tc::mma_commit(&sm.drain[0]);
     __syncwarp();
     if (!tc::mbar_wait(&sm.drain[0], 0) && lane == 0) atomicExch(&sm.abort_flag, 1);

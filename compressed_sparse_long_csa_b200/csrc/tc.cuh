@@ -53,6 +53,15 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 // Every wait of the library gives up after this long (a healthy wait takes microseconds).
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+// The loads armed on one barrier, in order, a phase each.  A role that leaves, early or not, waits for
+// the last one that it armed: the phase after it never completes, and while the last one is in flight a
+// wait on that next phase's parity returns at once (the phase before the last has the same parity).
+struct ArmedLoads {
+  int n = 0;
+  __host__ __device__ void arm() { ++n; }
+  __host__ __device__ bool any() const { return n > 0; }
+  __host__ __device__ uint32_t last() const { return (uint32_t)(n - 1) & 1u; }        // its phase's parity
+};
 // Bounded wait on a phase of a CTA-local mbarrier: false once limit_ns have passed.
 __device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
