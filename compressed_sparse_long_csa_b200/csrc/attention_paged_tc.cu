@@ -638,9 +638,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       if (seg.whole) {
         M = fmaxf(sink, m);
         float e = 0.f;
-        if (M != -INFINITY) {
+        if (M != -INFINITY || l != 0.f) {             // (logits that are all NaN have no maximum, but a sum)
           e = m == -INFINITY ? 0.f : __expf(m - M);
-          den = __expf(sink - M) + l * e;
+          den = (sink == -INFINITY ? 0.f : __expf(sink - M)) + l * e;
         }
         f = den > 0.f ? e / den : 0.f;
       }

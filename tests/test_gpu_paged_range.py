@@ -123,3 +123,17 @@ def test_large_values_at_a_maximum_that_rises(nats, lens, dtype, H, dk, dv):
         c.put(b, at, dk - 1, nats)
     c.run()
     c.check(nats)
+
+
+@pytest.mark.parametrize("dtype,H,dk,dv", SHAPES)
+@pytest.mark.parametrize("sink", [-math.inf, 0.5])
+@pytest.mark.parametrize("lens", [[1, 40, 64], [9000, 70]])
+def test_rows_of_nan_alone(lens, sink, dtype, H, dk, dv):
+    """Every attended row is NaN: so are all outputs, with or without a sink, cut or not."""
+    c = Plain(29, dtype, H, dk, dv, lens + [50], sink=sink)
+    for b, n in enumerate(lens):
+        c.put(b, torch.arange(n), slice(0, dk), math.nan)
+    c.run()
+    for b in range(len(lens)):
+        assert bool(c.out[b].isnan().all()) and bool(c.lse[b].isnan().all()), b
+    assert bool(c.out[-1].isfinite().all()) and bool(c.lse[-1].isfinite().all())
