@@ -265,12 +265,8 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
       }
       if (seg.whole) {
         const float sk = a.sink[h], top = fmaxf(sk, M);
-        float den = 0.f, f = 0.f;
-        if (top != -INFINITY || l != 0.f) {
-          f = M == -INFINITY ? 0.f : __expf(M - top);
-          den = (sk == -INFINITY ? 0.f : __expf(sk - top)) + l * f;
-        }
-        const float inv = den > 0.f ? f / den : 0.f;
+        const float f = M == -INFINITY ? 0.f : __expf(M - top), den = paged_sink(sk, top) + l * f;
+        const float inv = den == 0.f ? 0.f : f / den;
         T* dst = (T*)a.out + ((size_t)b * a.H + h) * dv + c;
         Elem<T>::st(dst, y.x * inv);
         Elem<T>::st(dst + 1, y.y * inv);
@@ -415,8 +411,8 @@ paged_merge_kernel(PagedAttnArgs a) {
       }
       den += __shfl_xor_sync(0xffffffffu, den, 8);
       den += __shfl_xor_sync(0xffffffffu, den, 16);
-      den += sk == -INFINITY ? 0.f : __expf(sk - M);
-      const float inv = den > 0.f ? 1.f / den : 0.f;
+      den += paged_sink(sk, M);
+      const float inv = den == 0.f ? 0.f : 1.f / den;
       float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 1
       for (int p0 = 0; p0 < n; p0 += 4) {
@@ -485,10 +481,10 @@ paged_merge_kernel(PagedAttnArgs a) {
     for (int o = PM_H; o < 32; o <<= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     if (lane < PM_H) red[1][warp][lane] = den;
     __syncthreads();
-    den = sk == -INFINITY ? 0.f : __expf(sk - M);
+    den = paged_sink(sk, M);
 #pragma unroll
     for (int w = 0; w < PM_THREADS / 32; ++w) den += red[1][w][hl];
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
     for (int c = c0; c - jc < cend; c += gw) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < cend) {

@@ -637,12 +637,9 @@ paged_attn_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant_
       float* blk = a.part + (size_t)seg.slot(unit) * paged_part_block(a.H, 512);
       if (seg.whole) {
         M = fmaxf(sink, m);
-        float e = 0.f;
-        if (M != -INFINITY || l != 0.f) {             // (logits that are all NaN have no maximum, but a sum)
-          e = m == -INFINITY ? 0.f : __expf(m - M);
-          den = (sink == -INFINITY ? 0.f : __expf(sink - M)) + l * e;
-        }
-        f = den > 0.f ? e / den : 0.f;
+        const float e = m == -INFINITY ? 0.f : __expf(m - M);
+        den = paged_sink(sink, M) + l * e;            // (logits that are all NaN have no maximum, but a sum)
+        f = den == 0.f ? 0.f : e / den;
       }
       const int d0 = 256 * wg + 128 * half;
       if (!seg.whole && hv && wg == 0 && half == 0) *reinterpret_cast<float2*>(blk + paged_part_rec(a.H, 512, h)) = make_float2(m, l);

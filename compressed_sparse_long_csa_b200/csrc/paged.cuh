@@ -236,6 +236,12 @@ __device__ __forceinline__ int64_t paged_row(const PagedAttnArgs& a, int b, int 
   return (int64_t)id * a.page + (e - pg * a.page);
 }
 
+// The sink's share of the denominator, e^{sink - M} with M = max(sink, ...): exact where the sink is the
+// maximum, so that an infinite one takes all of the probability; a NaN shows.
+__device__ __forceinline__ float paged_sink(float sink, float M) {
+  return sink == M ? (sink == -INFINITY ? 0.f : 1.f) : __expf(sink - M);
+}
+
 // Units of an attention launch over `ctas` CTAs per head group: no more than the tiles that
 // the shapes allow, so that a short context launches few CTAs.
 inline int paged_units(int ctas, int B, int64_t rows_max, int tile, int min_tiles) {

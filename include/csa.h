@@ -544,7 +544,8 @@ csa_status sparse_attn_decode_noalloc(const void* q, const void* cache, const in
  *   other arguments, and the results, as in those calls; a sequence without entries and
  *   window rows gives out = 0 and lse = sink.  Rows whose entry or page id is out of range
  *   are skipped and set CSA_DEVERR_INDEX.  Values of rows that are not attended (the rest of
- *   a sequence's last page, unused window rows) have no effect, whatever they hold.
+ *   a sequence's last page, unused window rows) have no effect, whatever they hold.  A NaN in an
+ *   attended row or in a head's sink shows in out and lse; a sink of +inf gives out = 0, lse = +inf.
  *   workspace >= attn_decode_paged_workspace_size(B, H, d_v, rows_max) bytes with rows_max =
  *   table_width * page_size + W (dense) or k + W (sparse).  Its contents need not be kept or
  *   cleared between calls; calls that may overlap on the GPU need workspaces of their own.

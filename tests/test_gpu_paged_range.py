@@ -36,7 +36,7 @@ class Plain(Case):
 
     def put(self, b, ids, dims, x):
         """rows[ids][:, dims] = x of sequence b"""
-        assert 0 <= int(ids.min()) and int(ids.max()) < self.lens[b]
+        assert all(0 <= i < self.lens[b] for i in ids.flatten().tolist())
         ids = ids.cuda()
         self.pages[self.table[b].long()[ids // 64], ids % 64, dims] = x if isinstance(x, float) else x.to(self.pages)
 
@@ -137,3 +137,19 @@ def test_rows_of_nan_alone(lens, sink, dtype, H, dk, dv):
     for b in range(len(lens)):
         assert bool(c.out[b].isnan().all()) and bool(c.lse[b].isnan().all()), b
     assert bool(c.out[-1].isfinite().all()) and bool(c.lse[-1].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype,H,dk,dv", SHAPES)
+@pytest.mark.parametrize("lens", [[1, 40, 0, 64], [9000, 0, 70], [1500] * 10])
+def test_sinks_of_infinity_and_nan(lens, dtype, H, dk, dv):
+    """A sink of +inf takes all of the probability: out = 0, lse = inf.  A NaN shows in its head alone."""
+    c = Plain(31, dtype, H, dk, dv, lens, sink=0.25)
+    c.sink[0], c.sink[2] = math.inf, math.nan
+    c.run()
+    assert bool((c.out[:, 0] == 0).all()) and bool((c.lse[:, 0] == math.inf).all())
+    for b, n in enumerate(lens):
+        assert bool(c.lse[b, 2].isnan())
+        assert bool(c.out[b, 2].isnan().all()) if n else bool((c.out[b, 2] == 0).all())
+    keep = [h for h in range(H) if h not in (0, 2)]
+    c.out, c.lse, c.q, c.sink = c.out[:, keep], c.lse[:, keep], c.q[:, keep], c.sink[keep]
+    c.check("other heads")
