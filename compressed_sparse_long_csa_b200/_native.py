@@ -79,10 +79,16 @@ def _p(t):
     return t.data_ptr()
 
 
+# The current device and its current stream's address without what the public calls add (a Stream
+# object a call: 3 us; a look for an initialised context).  These names are torch's own: where a
+# version has no such name, the public calls serve.
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
-        # the address alone (torch.cuda.current_stream() builds a Stream object: 3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _stream_now(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -325,8 +331,6 @@ def sparse_attn_decode_noalloc(q, cache, idx, win, win_len, sink, sm_scale, d_v,
 # checks are plain comparisons, written out (a helper per tensor cost 2 us a call); the message
 # is made when one fails.
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
-_device_now = torch._C._cuda_getDevice      # (torch.cuda.current_device looks for an initialised context first)
-_stream_now = torch._C._cuda_getCurrentRawStream
 
 
 def _unfit(name, what, t, want):
