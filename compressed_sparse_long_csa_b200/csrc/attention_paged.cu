@@ -19,7 +19,7 @@ namespace {
 constexpr int PC_ROWS = 32;      // rows per tile: one lane per row in the logits
 constexpr int PC_WARPS = 8;
 constexpr int PC_HEADS = 8;      // heads per CTA
-constexpr int PC_MIN_TILES = 1;  // (2: five sequences of up to 3001 rows of 64 dims 11.2 -> 13.5 us)
+constexpr int PC_MIN_TILES = 1;  // (2: five sequences of up to 3001 rows of 64 dims 11.2 -> 13.6 us)
 constexpr int PC_SMEM = 96 * 1024;     // two CTAs per SM
 
 __device__ __forceinline__ void cp_async16_zfill(void* dst, const void* src, bool zero) {
@@ -294,10 +294,10 @@ paged_attn_cc_kernel(PagedAttnArgs a, int bufs, int log_g) {
 // on the order in which the units ended.  Bound: latency (the notes, the records, the partials:
 // three round trips and the launch, 4 to 6 us behind the attention) and the L2, 4 H (dv + 4)
 // bytes per piece.  Sequences of few partials are a warp's work, so that many of them run at
-// once (32 ragged sequences 109.5 us without, 106.3 with; sparse, 48 sequences 58.7 against 55.9).
+// once (32 ragged sequences 102.7 us without, 98.5 with; sparse, 48 sequences 55.6 against 51.5).
 constexpr int PM_THREADS = 256, PM_H = 8, PM_C = PM_THREADS / PM_H, PM_SLICES = 16;
 constexpr int PM_EARLY = 5;      // partials on their way at once (9: two sequences of 131 072 rows, 64 heads 71.3 -> 71.9 us)
-constexpr int PM_PER_SM = 2;     // (1: 32 ragged sequences 105.0 -> 107.5 us)
+constexpr int PM_PER_SM = 2;     // (1: 32 ragged sequences 98.5 -> 103.2 us)
 constexpr int PM_FEW = 8;        // partials that one warp joins by itself (4: 32 ragged sequences 98.9 -> 100.4 us)
 constexpr int PM_ROUNDS = 2;     // notes of a thread: up to 512 units
 // Shared memory per unit (under the 48 KB of a plain launch for the 296 units that fp32 may have)

@@ -21,19 +21,22 @@
 // The MMAs are the weight-stationary form at M = 64: O (64 x 512) takes 128 lanes x 256 columns
 // and S 128 lanes x 32 columns, so lane l and lane l + 64 hold halves of the same head.
 // At a segment's end O is normalised and stored, or left as a partial for the merge.
-// Every wait is bounded (CSA_DEVERR_TIMEOUT).
+// Every wait on an mbarrier is bounded (CSA_DEVERR_TIMEOUT).  The named barriers between the lookup and
+// the copying warps have no limit; all of these warps take every one of them: a copying warp that is to
+// stop writes ld_stop before the barrier of a tile, all six read it behind that barrier and leave at
+// the same tile, and what a warp does between two barriers waits on mbarriers only.
 //
-// Bound: at 64 heads HBM (two sequences of up to 131 072 rows: 70 us, 4.1 TB/s of 6.56 measured,
+// Bound: at 64 heads HBM (two sequences of up to 131 072 rows: 71 us, 4.1 TB/s of 6.56 measured,
 // start and merge included), at 128 heads the MMAs and the shared memory that they read (2432
-// cycles of MMAs a tile; 32 ragged sequences: 95.6 us, 740 TFLOP/s, 1.9 us a tile, of which a
-// tile's chain load 1.1 us, S 0.7, softmax 0.9, PV 0.8 is overlapped by two), for gathered rows
-// the gathers (48 x 1152 rows: 48.4 us, 2.4 us a tile: 30 GB/s beside the MMAs' operands, 55
-// alone), for one sequence latency (100 rows: 11.2 us).
-// Two slots for all dims and all queries in shared memory: 105 us ragged, 73.5 us for 64 heads.
+// cycles of MMAs a tile; 32 ragged sequences of 200 296 rows in all: 98.5 us, 566 TFLOP/s, 1.9 us a
+// tile, of which a tile's chain load 1.1 us, S 0.7, softmax 0.9, PV 0.8 is overlapped by two), for
+// gathered rows the gathers (48 x 1152 rows: 51.4 us, 2.4 us a tile: 30 GB/s beside the MMAs' operands, 55
+// alone), for one sequence latency (100 rows: 11.5 us).
+// Two slots for all dims and all queries in shared memory: 10% more for the ragged ones, 5% for 64 heads.
 // Why 64 heads a CTA: O of 128 heads (512 columns) would leave no TMEM for S.  Why two bf16
-// parts of P: one part took 64 heads from 80 to 76 us when that was tried, for the error above.
-// Why few warps poll: all copying warps waiting on the slots' barriers made the ragged batch
-// 100 us, one thread and a named barrier 95.6; each test of a barrier goes through the shared
+// parts of P: one part took 5% off 64 heads when that was tried, for the error above.
+// Why few warps poll: all copying warps waiting on the slots' barriers cost the ragged batch
+// 5% against one thread and a named barrier; each test of a barrier goes through the shared
 // memory that the MMAs read.
 #include "paged.cuh"
 #include "tc.cuh"
@@ -55,8 +58,8 @@ constexpr int PT_LDW = 10;               // the warp that looks rows up
 constexpr int PT_CPW = 11;               // first of five that copy them
 constexpr int PT_CPT = 160, PT_LDT = 32 + PT_CPT;           // threads of the latter; of both
 constexpr int PT_THREADS = PT_CPW * 32 + PT_CPT;
-constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 11.3 us in one unit, 13.5 in two and a merge)
-constexpr int PT_BEGIN_COST = 2;         // (32 ragged sequences: 98.1 us at 1, 95.6 at 2, 97.9 at 3)
+constexpr int PT_MIN_TILES = 2;         // (one sequence of two tiles: 11.6 us in one unit, 13.5 in two and a merge)
+constexpr int PT_BEGIN_COST = 2;         // (32 ragged sequences: 100.8 us at 1, 98.5 at 2, 99.8 at 3)
 constexpr float PT_RESCALE = 8.0f;       // base-2 units: O is rescaled once the maximum has grown 256-fold
 constexpr int ATOM = PT_ROWS * 128;      // one 64-row x 128-byte swizzle atom
 constexpr int PT_QT = 6;                 // atoms of the queries that live in TMEM

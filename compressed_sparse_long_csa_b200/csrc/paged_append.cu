@@ -5,8 +5,10 @@
 // position (partial rotary embedding).  A pair (a, b) of the rotated dims at position p with
 // frequency f becomes (a cos t - b sin t, a sin t + b cos t), t = p f.
 //
-// Bound: HBM for chunks (each new row and rotary part read and written once), launch and
-// load latency for single tokens.  A CTA takes one token and a share of its heads.
+// Bound: launch and load latency for single tokens; for chunks the loads that are in flight (a CTA
+// loads, waits and stores): 4096 tokens of 128 heads 32.7 us, 4.3 TB/s of 6.56 measured, and 30.7 with
+// query rows of the rotary part alone, so that where the rows are written is a small part of it.  A CTA
+// takes one token and a share of its heads.
 #include <type_traits>
 
 #include "common.cuh"
@@ -20,8 +22,10 @@ constexpr int PA_THREADS = 128;
 // Query pieces that a thread loads first of all, and the heads of a CTA: few of both while the
 // grid does not fill the GPU (latency), many once it does (a token's entry, page and angles are
 // then looked up once).  bf16, 128 heads: 160 tokens 3.8 us against 5.0 the other way, 400
-// tokens 7.5 against 6.4; 4096 tokens 32.8 us (4.3 TB/s; every ninth line of the query rows is written).
-constexpr int PA_FEW = 1, PA_MANY = 8;   // (4: 35.4, 16: 38.4 us for the 4096; two pieces of 32 heads: one token 2.8 us, not 2.4)
+// tokens 7.5 against 6.4.  Many is as measured for 128 heads of 64 rotated dims in bf16, neighbouring
+// pairs: 8 pieces a thread (4096 tokens 32.7 us; 4: 35.4, 16: 38.4).  Pairs of halves have 4 such
+// pieces and leave half of the slots unused (35.6 us), fp32 has 16 (55.9 us, halves 52.3).
+constexpr int PA_FEW = 1, PA_MANY = 8;   // (few, two pieces of 32 heads: one token 2.8 us, not 2.4)
 constexpr int PA_FEW_HEADS = 16;
 
 struct AppendArgs {
@@ -30,7 +34,7 @@ struct AppendArgs {
   const float* inv_freq; int dr;
   void* pages; int64_t n_pages; int page;
   const int32_t* table; int table_w;
-  int B, T, d;
+  int B, d;
   const void* q_pe; int64_t qpe_ld_t, qpe_ld_h;
   void* q; int H, dq;
   int heads;                           // heads per CTA
@@ -39,7 +43,10 @@ struct AppendArgs {
 
 // cos and sin of pos * f.  The angle reaches 1e6 and more, where fp32 would lose its
 // fraction of a turn: the product (exact to 2^-53) and its reduction to [-1/2, 1/2] turns
-// are fp64, the functions of the reduced angle fp32.
+// are fp64.  The reduced angle is then rounded to fp32 (up to 2^-25 of half a turn) and the functions
+// are fp32 ones: the narrow fp64 pipe would cost a single token more than its launch.  An fp32 row's
+// error is 1.3 times that of cos and sin formed in 64 bits (3.9e-8 against 3.0e-8 relative to
+// the rotated rows); a bf16 row's is its own rounding's.
 __device__ __forceinline__ void turn(int pos, float f, float* c, float* s) {
   const double r = (double)pos * (double)f * 0.15915494309189533577;   // turns
   sincospif((float)(2.0 * (r - rint(r))), s, c);
@@ -152,7 +159,7 @@ cudaError_t launch_latent_append_paged(const void* rows, int64_t rows_ld, const 
                                        int64_t n_pages, int page, const int32_t* table, int table_w, int B, int T,
                                        int d, const void* q_pe, int64_t qpe_ld_t, int64_t qpe_ld_h, void* q, int H,
                                        int dq, int dtype, cudaStream_t st, unsigned* err) {
-  AppendArgs a{rows, rows_ld, seq, entry, pos, inv_freq, dr, pages, n_pages, page, table, table_w, B, T, d,
+  AppendArgs a{rows, rows_ld, seq, entry, pos, inv_freq, dr, pages, n_pages, page, table, table_w, B, d,
                q_pe, qpe_ld_t, qpe_ld_h, q, H, dq, q ? H : 1, err};
   const bool few = q && (int64_t)T * ((H + PA_FEW_HEADS - 1) / PA_FEW_HEADS) <= 12 * num_sms();
   if (few && H > PA_FEW_HEADS) a.heads = PA_FEW_HEADS;

@@ -36,7 +36,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
-// One test, without the suspension of try_wait: for a warp that polls several barriers.
+// One test, without the suspension of try_wait: whether something has already happened, so that the
+// wait for it later can be left out.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(

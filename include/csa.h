@@ -550,7 +550,9 @@ csa_status sparse_attn_decode_noalloc(const void* q, const void* cache, const in
  *   table_width * page_size + W (dense) or k + W (sparse).  Its contents need not be kept or
  *   cleared between calls; calls that may overlap on the GPU need workspaces of their own.
  * The work of a call follows the lengths found on the device, not the table's width, and
- * is dealt evenly over the SMs however ragged the lengths are.
+ * is dealt evenly over the SMs however ragged the lengths are.  Sequences without a row that
+ * lie between two others are passed one by one, 0.08 us (CUDA cores) to 0.28 us (tensor cores)
+ * each (65 533 of them: 5 and 18 ms).
  * Supported: H <= 128, d_v <= d_k <= 576, d_k % 8 == 0, d_v % 4 == 0, W <= 4096, k <= 65536.
  * ------------------------------------------------------------------------- */
 csa_status latent_append_paged(const void* rows, int64_t rows_ld, const int32_t* seq, const int32_t* entry,
