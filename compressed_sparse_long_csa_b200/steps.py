@@ -121,7 +121,7 @@ def _place_fresh(T, p, stream):
     entry0 = T[p + "entry0"]
     on = contextlib.nullcontext()
     if stream is not None:
-        on = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+        on = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(N._stream(stream)))
     with on:
         if p + "fresh_row" in T:
             # the CSA pooling takes its entry's index from where it writes (entry 0 has no block

@@ -3,6 +3,8 @@ n_entries and q_pos written in place between steps, eager and as a replayed grap
 the pages hold what the contiguous steps' cache holds, bit for bit."""
 from __future__ import annotations
 
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -87,21 +89,23 @@ def test_the_position_moves_on(wid, scale, page, captured):
         same(A, P, D, wl.kind, (i, entries))
 
 
-@pytest.mark.parametrize("how", ["stream", "address"])
+@pytest.mark.parametrize("how", ["stream", "address", "holder", "null"])
 def test_on_another_stream(how):
-    """The step's device operations all run on the stream that it is given."""
+    """The step's device operations all run on the stream that it is given: a torch stream, an address,
+    an object that has one, the null stream."""
     wl = CI.make_workload(2, scale={"B": 2, "T": 128 * 100})
     D = wl.dims
     A, P = steps.upload(wl), steps.upload(wl)
     steps.page_caches(P, D, wl.kind, 16)
-    s = torch.cuda.Stream()
+    s = torch.cuda.default_stream() if how == "null" else torch.cuda.Stream()
+    given = {"stream": s, "address": s.cuda_stream, "holder": SimpleNamespace(cuda_stream=s.cuda_stream), "null": 0}[how]
     torch.cuda.synchronize()
     for entries in ((3, 4), (4, 16)):
         for T in (A, P):
             move(T, D, wl.kind, entries)
         steps.run_step(wl.kind, A, D)
         torch.cuda.synchronize()
-        steps.run_step(wl.kind, P, D, stream=s if how == "stream" else s.cuda_stream)
+        steps.run_step(wl.kind, P, D, stream=given)
         s.synchronize()
         same(A, P, D, wl.kind, entries)
     assert csa.read_device_error() == 0
